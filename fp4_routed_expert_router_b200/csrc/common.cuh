@@ -11,7 +11,7 @@ namespace moe {
 // (expert / layer / byte index), [2] kernel id, [3] reserved.
 enum : int { ERR_OK = 0, ERR_EINVAL = 1, ERR_ESLOT = 4, ERR_ETIMEOUT = 5 };
 enum : int { KID_ROUTE = 1, KID_LOAD = 2, KID_UP = 3, KID_DOWN = 4, KID_COMBINE = 5,
-             KID_TC_UP = 6, KID_TC_DOWN = 7, KID_GATHER = 8 };
+             KID_TC_UP = 6, KID_TC_DOWN = 7, KID_GATHER = 8, KID_LINEAR = 9 };
 
 __device__ __forceinline__ void latch_error(int* err, int code, int detail, int kid) {
     if (atomicCAS(err, 0, code) == 0) {

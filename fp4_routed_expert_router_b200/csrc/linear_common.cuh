@@ -1,0 +1,133 @@
+// linear_common.cuh -- what the 16-bit product kernels share: arguments,
+// element conversions, activations and the finishing step of an output value.
+//
+// Three products per layer, with x [R, K], w [N, K], dz [R, N]:
+//   forward  y[r][n]  = act(sum_k x[r][k] w[n][k] + b[n]) + residual[r][n]
+//   dgrad    dx[r][k] = sum_n dz[r][n] w[n][k]  (+ dz_up, w_up)
+//   wgrad    dw[n][k] = sum_r dz[r][n] x[r][k]
+// All three write a row-major out[row][c].  The operand that runs along c (w,
+// w, x) is called A and the one that runs along the rows (x, dz, dz) B, so that
+// one kernel serves all: out[row][c] = sum_q A(q, c) B(q, row).  Groups (experts)
+// split the rows of the forward and of dgrad, and the sum of wgrad.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+enum : int { LIN_BF16 = 0, LIN_F16 = 1, LIN_F32 = 2 };
+enum : int { LACT_NONE = 0, LACT_RELU = 1, LACT_SILU = 2, LACT_GELU = 3, LACT_SWIGLU = 4 };
+enum : int { LIN_FWD = 0, LIN_DGRAD = 1, LIN_WGRAD = 2 };
+
+constexpr int kLinMaxGroups = 1024;
+
+struct LinArgs {
+    const int32_t* offsets;   // [E+1] or NULL: one group holding rows [0, rows)
+    int E;                    // groups (1 when offsets is NULL)
+    int rows;                 // R
+    int C;                    // length of an output row
+    int Q;                    // terms of the sum (forward K, dgrad N; wgrad: the group's rows)
+    int out_n;                // output rows of a group (wgrad N; else unused)
+    int kind, type, act;
+    // A: weights (a[1]: the second weight of SwiGLU) or, for wgrad, x
+    const void* a[2];
+    long long lda, a_gstride;
+    // B: x, dz and dz_up, or for wgrad dz and dz_up (two outputs)
+    const void* b[2];
+    long long ldb;
+    const int32_t* gather;    // rows of x: of B (forward) or of A (wgrad), or NULL
+    int gather_total;
+    // output
+    void* out[2];
+    long long ldo, o_gstride;
+    int out_type;
+    const int32_t* scatter;   // output row of grouped row i, or NULL
+    int scatter_total;
+    const void* bias[2];
+    int bias_type;
+    const void* res;          // added after the activation (wgrad: the old output with `accumulate`)
+    long long ldr;
+    int res_type;
+    int accumulate;
+    void* z[2];
+    long long ldz;
+    int* err;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ float lin_load(const void* p, size_t i, int type) {
+    if (type == LIN_F32) return static_cast<const float*>(p)[i];
+    const uint16_t v = static_cast<const uint16_t*>(p)[i];
+    return type == LIN_BF16 ? bf16_to_f32(v) : __half2float(__ushort_as_half(v));
+}
+
+__device__ __forceinline__ uint16_t lin_cvt16(float v, int type) {
+    return type == LIN_BF16 ? f32_to_bf16_rne(v) : __half_as_ushort(__float2half_rn(v));
+}
+
+__device__ __forceinline__ void lin_store(void* p, size_t i, float v, int type) {
+    if (type == LIN_F32) static_cast<float*>(p)[i] = v;
+    else static_cast<uint16_t*>(p)[i] = lin_cvt16(v, type);
+}
+
+__device__ __forceinline__ float lin_act(int act, float z, float z_up) {
+    switch (act) {
+        case LACT_RELU: return z > 0.0f || z != z ? z : 0.0f;   // NaN stays NaN
+        case LACT_SILU: return z / (1.0f + expf(-z));
+        case LACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        case LACT_SWIGLU: return z / (1.0f + expf(-z)) * z_up;
+        default: return z;
+    }
+}
+
+// d act / d z of relu, silu (also the gate of SwiGLU) and gelu.
+__device__ __forceinline__ float lin_slope(int act, float z) {
+    if (act == LACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    if (act == LACT_GELU)
+        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    const float s = 1.0f / (1.0f + expf(-z));
+    return s * (1.0f + z * (1.0f - s));
+}
+
+// Rows [p0, p1) of group e; false (and EINVAL) when they are no part of [0, rows].
+__device__ __forceinline__ bool lin_group(const int32_t* offsets, int rows, int e, int* err, int* p0, int* p1) {
+    if (!offsets) {
+        *p0 = 0;
+        *p1 = rows;
+        return true;
+    }
+    const int o0 = __ldg(offsets + e), o1 = __ldg(offsets + e + 1);
+    *p0 = o0;
+    *p1 = o1;
+    if (o0 >= 0 && o0 <= o1 && o1 <= rows) return true;
+    *p1 = *p0 = 0;
+    latch_error(err, ERR_EINVAL, e, KID_LINEAR);
+    return false;
+}
+
+// Source row of grouped row r through an index array, -1 (and EINVAL) when the index is out of range.
+__device__ __forceinline__ int lin_index(const int32_t* idx, int total, int r, int* err) {
+    if (!idx) return r;
+    const int v = __ldg(idx + r);
+    if (v >= 0 && v < total) return v;
+    latch_error(err, ERR_EINVAL, r, KID_LINEAR);
+    return -1;
+}
+
+// Finish one output value of the forward or dgrad: bias, activation, z, residual.
+// r: grouped row, orow: output row (-1: only z is written).
+__device__ __forceinline__ void lin_finish(const LinArgs& a, int e, int r, int orow, int c, float v, float u) {
+    const size_t bi = static_cast<size_t>(e) * a.C + c;
+    if (a.bias[0]) v += lin_load(a.bias[0], bi, a.bias_type);
+    if (a.bias[1]) u += lin_load(a.bias[1], bi, a.bias_type);
+    const size_t zi = static_cast<size_t>(r) * a.ldz + c;
+    if (a.z[0]) lin_store(a.z[0], zi, v, a.type);
+    if (a.z[1]) lin_store(a.z[1], zi, u, a.type);
+    if (orow < 0) return;
+    v = lin_act(a.act, v, u);
+    if (a.res) v += lin_load(a.res, static_cast<size_t>(orow) * a.ldr + c, a.res_type);
+    lin_store(a.out[0], static_cast<size_t>(orow) * a.ldo + c, v, a.out_type);
+}
+
+}  // namespace moe

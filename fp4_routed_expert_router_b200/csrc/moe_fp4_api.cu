@@ -16,6 +16,8 @@
 #include "common.cuh"
 #include "decode_common.cuh"
 #include "decode_mx.cuh"
+#include "linear_grad.cuh"
+#include "linear_simple.cuh"
 #include "router.cuh"
 #include "slot_layout.cuh"
 #include "residency.h"
@@ -235,6 +237,7 @@ const char* kernel_name(int kid) {
         case KID_TC_UP: return "tc_up";
         case KID_TC_DOWN: return "tc_down";
         case KID_GATHER: return "gather";
+        case KID_LINEAR: return "linear";
         default: return "?";
     }
 }
@@ -868,6 +871,302 @@ moe_fp4_status moe_fp4_last_error(moe_fp4_ctx* c, char* msg, size_t n) {
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Dense and grouped 16-bit products (moe_fp4_linear, moe_fp4_linear_backward).
+namespace {
+
+// The context's device, current for one call.
+struct DeviceScope {
+    int before = -1;
+    bool ok;
+    explicit DeviceScope(int dev) {
+        ok = cudaGetDevice(&before) == cudaSuccess && (before == dev || cudaSetDevice(dev) == cudaSuccess);
+        if (before == dev) before = -1;
+    }
+    ~DeviceScope() {
+        if (before >= 0) cudaSetDevice(before);
+    }
+};
+
+bool lin_type16(int t) { return t == MOE_FP4_BF16 || t == MOE_FP4_F16; }
+bool lin_type_any(int t) { return lin_type16(t) || t == MOE_FP4_F32; }
+bool lin_aligned(const void* p, int type) {
+    return (reinterpret_cast<uintptr_t>(p) & (type == MOE_FP4_F32 ? 3 : 1)) == 0;
+}
+
+// Sizes both calls share; what: the call's name in messages.
+moe_fp4_status lin_sizes(moe_fp4_ctx* c, const char* what, int rows, int K, int N, int type, int act, int n_groups,
+                         const int32_t* offsets) {
+    if (rows < 0 || K < 1 || N < 1)
+        return host_fail(c, MOE_FP4_EINVAL, "%s: rows %d / in_features %d / out_features %d", what, rows, K, N);
+    if (!lin_type16(type)) return host_fail(c, MOE_FP4_EINVAL, "%s: type %d is not 16-bit", what, type);
+    if (act < MOE_FP4_ACT_NONE || act > MOE_FP4_ACT_SWIGLU)
+        return host_fail(c, MOE_FP4_EINVAL, "%s: unknown activation %d", what, act);
+    if (n_groups < 0 || n_groups > kLinMaxGroups || (n_groups > 0) != (offsets != nullptr))
+        return host_fail(c, MOE_FP4_EINVAL, "%s: %d groups (at most %d), offsets with groups only", what, n_groups,
+                         kLinMaxGroups);
+    if (reinterpret_cast<uintptr_t>(offsets) & 3) return host_fail(c, MOE_FP4_EINVAL, "%s: offsets alignment", what);
+    return MOE_FP4_OK;
+}
+
+// Row stride (0: dense); negative when it is smaller than a row.
+int64_t lin_ld(int64_t ld, int64_t width) { return ld == 0 ? width : (ld >= width ? ld : -1); }
+
+// Groups' stride of a [E, rows, ld] tensor: the last row of a group may end before its stride does.
+int64_t lin_gs(int64_t gs, int64_t rows, int64_t ld, int64_t width) {
+    if (gs == 0) return rows * ld;
+    return gs >= (rows - 1) * ld + width ? gs : -1;
+}
+
+cudaError_t lin_run(moe_fp4_ctx* c, const char* name, const LinArgs& a, cudaStream_t s) {
+    const unsigned ct = static_cast<unsigned>((a.C + kLsTile - 1) / kLsTile);
+    if (a.kind == LIN_WGRAD) {
+        const unsigned outs = a.b[1] ? 2u : 1u;
+        return launch_k(c, name, lin_simple_kernel<false>,
+                        dim3(ct, static_cast<unsigned>((a.out_n + kLsTile - 1) / kLsTile), outs * a.E), dim3(256), 0,
+                        s, a);
+    }
+    const dim3 grid(ct, static_cast<unsigned>((a.rows + kLsTile - 1) / kLsTile + a.E - 1));
+    if (a.kind == LIN_FWD && a.a[1]) return launch_k(c, name, lin_simple_kernel<true>, grid, dim3(256), 0, s, a);
+    return launch_k(c, name, lin_simple_kernel<false>, grid, dim3(256), 0, s, a);
+}
+
+cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
+    const bool db = g.db[0] || g.db[1];
+    // rows a strip should hold: enough for the column sums' epilogue to be small beside the loads
+    const int per_group = g.E > 0 ? (g.rows + g.E - 1) / g.E : g.rows;
+    int strips = per_group / 256;
+    const int most = db ? 8 : 64;              // a portable cluster holds 8 CTAs
+    strips = strips < 1 ? 1 : strips > most ? most : strips;
+    auto vec_ok = [](const void* p, long long ld, int type) {
+        const uintptr_t step = type == LIN_F32 ? 4 : 8;
+        return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % step == 0;
+    };
+    bool vec = g.N % 8 == 0 && vec_ok(g.dy, g.lddy, g.dy_type) && vec_ok(g.dz[0], g.lddz, g.type) &&
+               vec_ok(g.dz[1], g.lddz, g.type) && vec_ok(g.z[0], g.ldz, g.type) && vec_ok(g.z[1], g.ldz, g.type);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((g.N + kLgCols - 1) / kLgCols), static_cast<unsigned>(strips),
+                       static_cast<unsigned>(g.E));
+    cfg.blockDim = dim3(kLgThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = static_cast<unsigned>(strips);
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = db ? 2 : 1;
+    const bool prof = c->profile && c->prof.size() < 65536;
+    cudaEvent_t ea = nullptr, eb = nullptr;
+    if (prof) {
+        ea = take_event(c);
+        eb = take_event(c);
+        cudaEventRecord(ea, s);
+    }
+    const bool up = g.act == LACT_SWIGLU;
+    cudaError_t e = up ? (vec ? cudaLaunchKernelEx(&cfg, lin_grad_kernel<8, true>, g)
+                              : cudaLaunchKernelEx(&cfg, lin_grad_kernel<1, true>, g))
+                       : (vec ? cudaLaunchKernelEx(&cfg, lin_grad_kernel<8, false>, g)
+                              : cudaLaunchKernelEx(&cfg, lin_grad_kernel<1, false>, g));
+    if (prof) {
+        cudaEventRecord(eb, s);
+        c->prof.push_back({"linear_dz", ea, eb});
+    }
+    return e;
+}
+
+}  // namespace
+
+extern "C" moe_fp4_status moe_fp4_linear(moe_fp4_ctx* c, const moe_fp4_linear_args* p, void* stream) {
+    if (!c) return MOE_FP4_EINVAL;
+    if (!p) return host_fail(c, MOE_FP4_EINVAL, "linear: NULL arguments");
+    moe_fp4_status st = lin_sizes(c, "linear", p->rows, p->in_features, p->out_features, p->type, p->act, p->n_groups,
+                                  p->offsets);
+    if (st != MOE_FP4_OK) return st;
+    const int K = p->in_features, N = p->out_features;
+    const bool gated = p->act == MOE_FP4_ACT_SWIGLU;
+    if (!lin_type_any(p->y_type) || (p->bias && !lin_type_any(p->bias_type)) ||
+        (p->bias_up && !lin_type_any(p->bias_type)) || (p->residual && !lin_type_any(p->residual_type)))
+        return host_fail(c, MOE_FP4_EINVAL, "linear: unknown y, bias or residual type");
+    if (gated != (p->w_up != nullptr) || (!gated && (p->bias_up || p->z_up)) || p->reserved)
+        return host_fail(c, MOE_FP4_EINVAL, "linear: w_up goes with ACT_SWIGLU, bias_up and z_up with w_up");
+    if (p->z_up && !p->z) return host_fail(c, MOE_FP4_EINVAL, "linear: z_up without z");
+    const int64_t ldx = lin_ld(p->ldx, K), ldw = lin_ld(p->ldw, K), ldy = lin_ld(p->ldy, N),
+                  ldr = lin_ld(p->ld_residual, N), ldz = lin_ld(p->ldz, N);
+    const int64_t gs = p->n_groups ? lin_gs(p->w_group_stride, N, ldw, K) : 0;
+    if (ldx < 0 || ldw < 0 || ldy < 0 || ldr < 0 || ldz < 0 || gs < 0)
+        return host_fail(c, MOE_FP4_EINVAL, "linear: a stride is smaller than what it steps over");
+    if (p->rows == 0) return MOE_FP4_OK;
+    if (!p->x || !p->w || !p->y) return host_fail(c, MOE_FP4_EINVAL, "linear: NULL x, w or y");
+    if ((p->x_rows && p->x_total < 1) || (p->y_rows && p->y_total < 1))
+        return host_fail(c, MOE_FP4_EINVAL, "linear: x_rows needs x_total, y_rows needs y_total");
+    if (!lin_aligned(p->x, p->type) || !lin_aligned(p->w, p->type) || !lin_aligned(p->w_up, p->type) ||
+        !lin_aligned(p->y, p->y_type) || !lin_aligned(p->bias, p->bias_type) ||
+        !lin_aligned(p->bias_up, p->bias_type) || !lin_aligned(p->residual, p->residual_type) ||
+        !lin_aligned(p->z, p->type) || !lin_aligned(p->z_up, p->type) || !lin_aligned(p->x_rows, MOE_FP4_F32) ||
+        !lin_aligned(p->y_rows, MOE_FP4_F32))
+        return host_fail(c, MOE_FP4_EINVAL, "linear: a pointer is not aligned to its element");
+    DeviceScope dev(c->device);
+    if (!dev.ok) return host_fail(c, MOE_FP4_ECUDA, "linear: device %d", c->device);
+    LinArgs a{};
+    a.offsets = p->offsets;
+    a.E = p->n_groups ? p->n_groups : 1;
+    a.rows = p->rows;
+    a.C = N;
+    a.Q = K;
+    a.kind = LIN_FWD;
+    a.type = p->type;
+    a.act = p->act;
+    a.a[0] = p->w;
+    a.a[1] = p->w_up;
+    a.lda = ldw;
+    a.a_gstride = gs;
+    a.b[0] = p->x;
+    a.ldb = ldx;
+    a.gather = p->x_rows;
+    a.gather_total = p->x_rows ? p->x_total : p->rows;
+    a.out[0] = p->y;
+    a.ldo = ldy;
+    a.out_type = p->y_type;
+    a.scatter = p->y_rows;
+    a.scatter_total = p->y_rows ? p->y_total : p->rows;
+    a.bias[0] = p->bias;
+    a.bias[1] = p->bias_up;
+    a.bias_type = p->bias_type;
+    a.res = p->residual;
+    a.ldr = ldr;
+    a.res_type = p->residual_type;
+    a.z[0] = p->z;
+    a.z[1] = p->z_up;
+    a.ldz = ldz;
+    a.err = c->d_err;
+    a.timeout_ns = c->timeout_ns;
+    const cudaError_t e = lin_run(c, "linear", a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MOE_FP4_OK : cuda_fail(c, e, "linear: launch");
+}
+
+extern "C" moe_fp4_status moe_fp4_linear_backward(moe_fp4_ctx* c, const moe_fp4_linear_grads* p, void* stream) {
+    if (!c) return MOE_FP4_EINVAL;
+    if (!p) return host_fail(c, MOE_FP4_EINVAL, "linear_backward: NULL arguments");
+    moe_fp4_status st = lin_sizes(c, "linear_backward", p->rows, p->in_features, p->out_features, p->type, p->act,
+                                  p->n_groups, p->offsets);
+    if (st != MOE_FP4_OK) return st;
+    const int K = p->in_features, N = p->out_features, R = p->rows;
+    const bool gated = p->act == MOE_FP4_ACT_SWIGLU, plain = p->act == MOE_FP4_ACT_NONE;
+    if ((p->dy_type != p->type && p->dy_type != MOE_FP4_F32) || (p->dx && !lin_type_any(p->dx_type)) ||
+        ((p->dw || p->dw_up) && !lin_type_any(p->dw_type)) || p->reserved)
+        return host_fail(c, MOE_FP4_EINVAL, "linear_backward: dy has the type of x or fp32; unknown dx or dw type");
+    if (!gated && (p->w_up || p->dw_up || p->db_up || p->dz_up || p->z_up))
+        return host_fail(c, MOE_FP4_EINVAL, "linear_backward: *_up tensors go with ACT_SWIGLU");
+    const int64_t lddy = lin_ld(p->lddy, N), ldz = lin_ld(p->ldz, N), ldx = lin_ld(p->ldx, K), ldw = lin_ld(p->ldw, K),
+                  lddz = lin_ld(p->lddz, N), lddx = lin_ld(p->lddx, K), lddw = lin_ld(p->lddw, K);
+    const int64_t gs = p->n_groups ? lin_gs(p->w_group_stride, N, ldw, K) : 0;
+    const int64_t dgs = p->n_groups ? lin_gs(p->dw_group_stride, N, lddw, K) : 0;
+    if (lddy < 0 || ldz < 0 || ldx < 0 || ldw < 0 || lddz < 0 || lddx < 0 || lddw < 0 || gs < 0 || dgs < 0)
+        return host_fail(c, MOE_FP4_EINVAL, "linear_backward: a stride is smaller than what it steps over");
+    const bool want_dx = p->dx && R > 0, want_dw = p->dw || p->dw_up, want_db = p->db || p->db_up;
+    const bool direct = plain && p->dy_type == p->type && !p->y_rows;   // dy serves as dz
+    if (R > 0) {
+        if (!p->dy) return host_fail(c, MOE_FP4_EINVAL, "linear_backward: NULL dy");
+        if (!plain && (!p->z || (gated && !p->z_up))) return host_fail(c, MOE_FP4_EINVAL, "linear_backward: NULL z");
+        if (want_dx && (!p->w || (gated && !p->w_up))) return host_fail(c, MOE_FP4_EINVAL, "linear_backward: NULL w");
+        if (want_dw && !p->x) return host_fail(c, MOE_FP4_EINVAL, "linear_backward: NULL x");
+        if (!direct && (want_dx || p->dw) && !p->dz)
+            return host_fail(c, MOE_FP4_EINVAL, "linear_backward: dz is needed here");
+        if (gated && (want_dx || p->dw_up) && !p->dz_up)
+            return host_fail(c, MOE_FP4_EINVAL, "linear_backward: dz_up is needed here");
+        if ((p->x_rows && p->x_total < 1) || (p->y_rows && p->y_total < 1) || (p->dx_rows && p->dx_total < 1))
+            return host_fail(c, MOE_FP4_EINVAL, "linear_backward: x_rows, y_rows and dx_rows need their totals");
+    }
+    if (!lin_aligned(p->dy, p->dy_type) || !lin_aligned(p->z, p->type) || !lin_aligned(p->z_up, p->type) ||
+        !lin_aligned(p->x, p->type) || !lin_aligned(p->w, p->type) || !lin_aligned(p->w_up, p->type) ||
+        !lin_aligned(p->dz, p->type) || !lin_aligned(p->dz_up, p->type) || !lin_aligned(p->dx, p->dx_type) ||
+        !lin_aligned(p->dw, p->dw_type) || !lin_aligned(p->dw_up, p->dw_type) || !lin_aligned(p->db, MOE_FP4_F32) ||
+        !lin_aligned(p->db_up, MOE_FP4_F32) || !lin_aligned(p->x_rows, MOE_FP4_F32) ||
+        !lin_aligned(p->y_rows, MOE_FP4_F32) || !lin_aligned(p->dx_rows, MOE_FP4_F32))
+        return host_fail(c, MOE_FP4_EINVAL, "linear_backward: a pointer is not aligned to its element");
+    DeviceScope dev(c->device);
+    if (!dev.ok) return host_fail(c, MOE_FP4_ECUDA, "linear_backward: device %d", c->device);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    const int E = p->n_groups ? p->n_groups : 1;
+    if ((!direct && (p->dz || p->dz_up) && R > 0) || want_db) {
+        LinGradArgs g{};
+        g.offsets = p->offsets;
+        g.E = E;
+        g.rows = R;
+        g.N = N;
+        g.type = p->type;
+        g.act = p->act;
+        g.dy_rows = p->y_rows;
+        g.dy_total = p->y_rows ? p->y_total : R;
+        g.dy_type = p->dy_type;
+        g.dy = p->dy;
+        g.lddy = lddy;
+        g.z[0] = plain ? nullptr : p->z;
+        g.z[1] = p->z_up;
+        g.ldz = ldz;
+        g.dz[0] = p->dz;
+        g.dz[1] = p->dz_up;
+        g.lddz = lddz;
+        g.db[0] = p->db;
+        g.db[1] = p->db_up;
+        g.accumulate = p->accumulate;
+        g.err = c->d_err;
+        if ((e = lin_grad_run(c, g, s)) != cudaSuccess) return cuda_fail(c, e, "linear_backward: dz launch");
+    }
+    LinArgs a{};
+    a.offsets = p->offsets;
+    a.E = E;
+    a.rows = R;
+    a.type = p->type;
+    a.b[0] = direct ? p->dy : p->dz;
+    a.b[1] = p->dz_up;
+    a.ldb = direct ? lddy : lddz;
+    a.C = K;
+    a.err = c->d_err;
+    a.timeout_ns = c->timeout_ns;
+    if (want_dx) {
+        LinArgs d = a;
+        d.kind = LIN_DGRAD;
+        d.Q = N;
+        d.a[0] = p->w;
+        d.a[1] = p->w_up;
+        d.lda = ldw;
+        d.a_gstride = gs;
+        d.out[0] = p->dx;
+        d.ldo = lddx;
+        d.out_type = p->dx_type;
+        d.scatter = p->dx_rows;
+        d.scatter_total = p->dx_rows ? p->dx_total : R;
+        if ((e = lin_run(c, "linear_dx", d, s)) != cudaSuccess) return cuda_fail(c, e, "linear_backward: dx launch");
+    }
+    if (want_dw) {
+        LinArgs d = a;
+        d.kind = LIN_WGRAD;
+        d.out_n = N;
+        d.a[0] = p->x;
+        d.lda = ldx;
+        d.gather = p->x_rows;
+        d.gather_total = p->x_rows ? p->x_total : R;
+        d.out[0] = p->dw;
+        d.out[1] = p->dw_up;
+        if (!p->dw) {   // only the second weight's gradient
+            d.b[0] = p->dz_up;
+            d.out[0] = p->dw_up;
+        }
+        if (!p->dw || !p->dw_up) d.b[1] = nullptr;
+        d.ldo = lddw;
+        d.o_gstride = dgs;
+        d.out_type = p->dw_type;
+        d.accumulate = p->accumulate;
+        if ((e = lin_run(c, "linear_dw", d, s)) != cudaSuccess) return cuda_fail(c, e, "linear_backward: dw launch");
+    }
+    return MOE_FP4_OK;
+}
 
 // ---------------------------------------------------------------------------
 // Forward without allocation (moe_fp4_forward_noalloc): the decode kernel

@@ -35,7 +35,10 @@
  * route, forward, route_forward, last_error (the layer); expert_outputs,
  * combine (the two halves of forward, for expert-parallel use); saliency
  * (per-expert statistic of the last forward); forward_noalloc (forward
- * without any allocation, library-owned static scratch).
+ * without any allocation, library-owned static scratch); linear,
+ * linear_backward (16-bit matrix products beside the FP4 experts -- router
+ * logits, shared experts, unquantised experts or adapters -- dense or grouped
+ * by expert, and their gradients).
  */
 #ifndef MOE_FP4_H
 #define MOE_FP4_H
@@ -384,6 +387,124 @@ moe_fp4_status moe_fp4_forward_noalloc(const moe_fp4_config *cfg, const uint8_t 
                                        int T, const float *weights, const int32_t *offsets,
                                        const int32_t *perm, float *y, uint16_t *x_out,
                                        int32_t *err, void *stream);
+
+/* Element types of moe_fp4_linear and moe_fp4_linear_backward. */
+enum { MOE_FP4_BF16 = 0, MOE_FP4_F16 = 1, MOE_FP4_F32 = 2 };
+/* Activations: identity, max(z, 0), z / (1 + e^-z), z * Phi(z) (the normal
+ * distribution function, erf form) and the gated silu(z) * z_up. */
+enum {
+    MOE_FP4_ACT_NONE = 0,
+    MOE_FP4_ACT_RELU = 1,
+    MOE_FP4_ACT_SILU = 2,
+    MOE_FP4_ACT_GELU = 3,
+    MOE_FP4_ACT_SWIGLU = 4
+};
+
+/*
+ * Arguments of moe_fp4_linear.  Zero the struct first; a row stride of 0
+ * means dense.  Strides count elements; the innermost stride is 1.
+ */
+typedef struct {
+    int32_t rows;              /* R: rows of the product, >= 0 (grouped rows when n_groups > 0) */
+    int32_t in_features;       /* K >= 1 */
+    int32_t out_features;      /* N >= 1 */
+    int32_t type;              /* x, w, w_up, z, z_up: MOE_FP4_BF16 or MOE_FP4_F16 */
+    int32_t act;               /* MOE_FP4_ACT_* */
+    int32_t n_groups;          /* E <= 1024: weights per group; 0: one weight for all rows */
+    const int32_t *offsets;    /* [E+1]: group e is rows [offsets[e], offsets[e+1]) (as from moe_fp4_route) */
+    const int32_t *x_rows;     /* [R] or NULL: row i reads x[x_rows[i]] instead of x[i] */
+    const int32_t *y_rows;     /* [R] or NULL: row i is written to y[y_rows[i]] (distinct) instead of y[i] */
+    int32_t x_total;           /* rows of x (with x_rows; else R) */
+    int32_t y_total;           /* rows of y and residual (with y_rows; else R) */
+    const void *x;             /* [x_total, K] */
+    const void *w;             /* [N, K], or [E, N, K] */
+    const void *w_up;          /* the same, SWIGLU only */
+    int64_t ldx, ldw;          /* row strides */
+    int64_t w_group_stride;    /* elements from one group's weight to the next (0: N * ldw) */
+    const void *bias;          /* [N] or [E, N] dense, or NULL */
+    const void *bias_up;       /* the same for w_up */
+    int32_t bias_type;         /* MOE_FP4_BF16, _F16 or _F32 */
+    int32_t residual_type;     /* MOE_FP4_BF16, _F16 or _F32 */
+    const void *residual;      /* [y_total, N] or NULL; may be y itself (same type and stride) */
+    int64_t ld_residual;
+    void *y;                   /* [y_total, N] out */
+    int64_t ldy;
+    int32_t y_type;            /* MOE_FP4_BF16, _F16 or _F32 */
+    int32_t reserved;          /* 0 */
+    void *z, *z_up;            /* [R, N] out or NULL: pre-activations in grouped order, for the backward pass */
+    int64_t ldz;
+} moe_fp4_linear_args;
+
+/*
+ * 16-bit matrix product with bias, activation and residual, dense or grouped
+ * by expert with ragged group sizes:
+ *   z = x w^T + bias        z_up = x w_up^T + bias_up      (SWIGLU only)
+ *   y = act(z) + residual   (SWIGLU: silu(z) * z_up + residual)
+ * Products accumulate in fp32, bias, activation and residual are applied in
+ * fp32 and y, z and z_up are rounded once.  With a fp32 y the accumulation is
+ * done in fp32 registers over spans of K of at most 640 (the tensor core
+ * truncates its fp32 sums, which costs about 1e-9 relative per K); 16-bit
+ * outputs do not need that.
+ * Grouped (n_groups > 0): row i of group e takes w[e], bias[e].  Rows of y and
+ * z outside every group are left as they were; an empty group does nothing.
+ * x_rows and y_rows fuse the gather of token rows into grouped order and the
+ * scatter of results into entry order ((offsets, perm) of moe_fp4_route:
+ * x_rows = perm / k, y_rows = perm).
+ * Any size, row stride and (natural) alignment is accepted.  The fast operand
+ * path needs x and w with 16-byte aligned bases and row strides that are
+ * multiples of 8 elements.
+ * No workspace is used: calls may overlap in time on different streams.
+ * Errors: EINVAL, ECUDA; latched: EINVAL (offsets that do not ascend inside
+ * [0, R]: that group is skipped; an x_rows entry outside [0, x_total): that
+ * row counts as zero; a y_rows entry outside [0, y_total): that row is not
+ * written), ETIMEOUT.
+ */
+moe_fp4_status moe_fp4_linear(moe_fp4_ctx *ctx, const moe_fp4_linear_args *args, void *stream);
+
+/* Arguments of moe_fp4_linear_backward (zero the struct first; strides as above). */
+typedef struct {
+    int32_t rows, in_features, out_features;   /* as in the forward */
+    int32_t type, act, n_groups;
+    const int32_t *offsets;
+    const int32_t *x_rows;     /* as in the forward: x is read through it */
+    const int32_t *y_rows;     /* as in the forward: dy is read through it */
+    const int32_t *dx_rows;    /* [R] or NULL: dx row of row i (distinct) */
+    int32_t x_total, y_total, dx_total;
+    int32_t dy_type;           /* type, or MOE_FP4_F32 */
+    const void *dy;            /* [y_total, N] */
+    int64_t lddy;
+    const void *z, *z_up;      /* [R, N] as kept by the forward; unused for ACT_NONE */
+    int64_t ldz;
+    const void *x, *w, *w_up;
+    int64_t ldx, ldw, w_group_stride;
+    void *dz, *dz_up;          /* [R, N] out in `type`: the gradients before the activation, rounded once; dz may
+                                  be NULL when act is NONE, dy has type `type` and no y_rows are given (dy is
+                                  used as it is); dz_up for SWIGLU only */
+    int64_t lddz;
+    void *dx;                  /* [dx_total (or R), K] out or NULL */
+    int64_t lddx;
+    int32_t dx_type;           /* MOE_FP4_BF16, _F16 or _F32 */
+    int32_t dw_type;
+    void *dw, *dw_up;          /* [N, K] or [E, N, K] out or NULL (dw_up: SWIGLU only) */
+    int64_t lddw, dw_group_stride;
+    float *db, *db_up;         /* [N] or [E, N] out or NULL */
+    int32_t accumulate;        /* nonzero: add to dw, dw_up, db, db_up instead of overwriting them */
+    int32_t reserved;          /* 0 */
+} moe_fp4_linear_grads;
+
+/*
+ * Gradients of moe_fp4_linear for a given dy (the residual's gradient is dy):
+ *   dz = dy * act'(z)       (SWIGLU: dz = dy z_up silu'(z), dz_up = dy silu(z))
+ *   dx = dz w + dz_up w_up,  dw = dz^T x,  dw_up = dz_up^T x,
+ *   db = sum over rows of dz (before its rounding, fp32, fixed order).
+ * dw and db of an empty group are zero (unchanged with `accumulate`).  With
+ * x_rows the gradient of a shared x row is the sum of its rows of dx, which
+ * dx_rows = perm puts where moe_fp4_combine adds them up.  dz and dz_up are
+ * the caller's buffers, so calls may overlap in time like moe_fp4_linear's.
+ * Rows outside every group are neither read nor written.
+ * Errors: as moe_fp4_linear (a bad y_rows entry counts as a zero dy row).
+ */
+moe_fp4_status moe_fp4_linear_backward(moe_fp4_ctx *ctx, const moe_fp4_linear_grads *args, void *stream);
 
 #ifdef __cplusplus
 }
