@@ -115,19 +115,10 @@ __device__ __forceinline__ int lin_index(const int32_t* idx, int total, int r, i
     return -1;
 }
 
-// Finish one output value of the forward or dgrad: bias, activation, z, residual.
-// r: grouped row, orow: output row (-1: only z is written).
-__device__ __forceinline__ void lin_finish(const LinArgs& a, int e, int r, int orow, int c, float v, float u) {
-    const size_t bi = static_cast<size_t>(e) * a.C + c;
-    if (a.bias[0]) v += lin_load(a.bias[0], bi, a.bias_type);
-    if (a.bias[1]) u += lin_load(a.bias[1], bi, a.bias_type);
-    const size_t zi = static_cast<size_t>(r) * a.ldz + c;
-    if (a.z[0]) lin_store(a.z[0], zi, v, a.type);
-    if (a.z[1]) lin_store(a.z[1], zi, u, a.type);
-    if (orow < 0) return;
-    v = lin_act(a.act, v, u);
-    if (a.res) v += lin_load(a.res, static_cast<size_t>(orow) * a.ldr + c, a.res_type);
-    lin_store(a.out[0], static_cast<size_t>(orow) * a.ldo + c, v, a.out_type);
+template <int ACT>
+__device__ __forceinline__ void lin_act16(float (&v)[16], const float (&u)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = lin_act(ACT, v[j], u[j]);
 }
 
 }  // namespace moe

@@ -17,7 +17,7 @@
 #include "decode_common.cuh"
 #include "decode_mx.cuh"
 #include "linear_grad.cuh"
-#include "linear_simple.cuh"
+#include "linear_tc.cuh"
 #include "router.cuh"
 #include "slot_layout.cuh"
 #include "residency.h"
@@ -258,6 +258,8 @@ cudaError_t launch_mx(const MxArgs& a, const SlotLayout& L, const MxPlan& p, int
     return cudaLaunchKernelEx(&cfg, moe_fp4_decode_mx, a, L, p);
 }
 
+cudaError_t lin_allow_smem(int bytes);
+
 cudaError_t allow_mx_smem(int bytes) {
     return cudaFuncSetAttribute(reinterpret_cast<const void*>(moe_fp4_decode_mx),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -431,7 +433,7 @@ moe_fp4_status moe_fp4_create(const moe_fp4_config* cfg, int device, void* arena
         return bail(MOE_FP4_ENOMEM);
     }
     mx_bind(&c->mx, c->d_mx, mo, mz.cnt);
-    if (allow_mx_smem(c->smem_optin) != cudaSuccess ||
+    if (allow_mx_smem(c->smem_optin) != cudaSuccess || lin_allow_smem(c->smem_optin) != cudaSuccess ||
         cudaMemset(c->d_mx, 0, mo.xp) != cudaSuccess) {   // sequence, counters, flags, zero block
         cudaGetLastError();
         return bail(MOE_FP4_ECUDA);
@@ -919,17 +921,40 @@ int64_t lin_gs(int64_t gs, int64_t rows, int64_t ld, int64_t width) {
     return gs >= (rows - 1) * ld + width ? gs : -1;
 }
 
+template <int KIND, bool DUAL>
+cudaError_t lin_launch(moe_fp4_ctx* c, const char* name, const LinArgs& a, const LtPlan& p, bool tma,
+                       const LtMaps& m, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(p.grid)), block(static_cast<unsigned>(lt_threads(tma)));
+    return tma ? launch_k(c, name, lin_tc_kernel<KIND, DUAL, true>, grid, block, p.smem, s, a, p, m)
+               : launch_k(c, name, lin_tc_kernel<KIND, DUAL, false>, grid, block, p.smem, s, a, p, m);
+}
+
 cudaError_t lin_run(moe_fp4_ctx* c, const char* name, const LinArgs& a, cudaStream_t s) {
-    const unsigned ct = static_cast<unsigned>((a.C + kLsTile - 1) / kLsTile);
-    if (a.kind == LIN_WGRAD) {
-        const unsigned outs = a.b[1] ? 2u : 1u;
-        return launch_k(c, name, lin_simple_kernel<false>,
-                        dim3(ct, static_cast<unsigned>((a.out_n + kLsTile - 1) / kLsTile), outs * a.E), dim3(256), 0,
-                        s, a);
+    const LtPlan p = lt_plan(a, c->sm_count, c->smem_optin);
+    if (p.stages < 2 || p.grid < 1) return cudaErrorInvalidConfiguration;
+    LtMaps m{};
+    const bool tma = lt_tma_ok(a);
+    if (tma && !lt_maps(a, p, &m)) return cudaErrorInvalidValue;
+    if (a.kind == LIN_WGRAD) return lin_launch<LIN_WGRAD, false>(c, name, a, p, tma, m, s);
+    if (a.kind == LIN_DGRAD) return lin_launch<LIN_DGRAD, false>(c, name, a, p, tma, m, s);
+    return a.a[1] ? lin_launch<LIN_FWD, true>(c, name, a, p, tma, m, s)
+                  : lin_launch<LIN_FWD, false>(c, name, a, p, tma, m, s);
+}
+
+cudaError_t lin_allow_smem(int bytes) {
+    const void* k[] = {reinterpret_cast<const void*>(lin_tc_kernel<LIN_FWD, false, true>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_FWD, false, false>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_FWD, true, true>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_FWD, true, false>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_DGRAD, false, true>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_DGRAD, false, false>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_WGRAD, false, true>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_WGRAD, false, false>)};
+    for (const void* f : k) {
+        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
     }
-    const dim3 grid(ct, static_cast<unsigned>((a.rows + kLsTile - 1) / kLsTile + a.E - 1));
-    if (a.kind == LIN_FWD && a.a[1]) return launch_k(c, name, lin_simple_kernel<true>, grid, dim3(256), 0, s, a);
-    return launch_k(c, name, lin_simple_kernel<false>, grid, dim3(256), 0, s, a);
+    return cudaSuccess;
 }
 
 cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
