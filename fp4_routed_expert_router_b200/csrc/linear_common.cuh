@@ -115,10 +115,10 @@ __device__ __forceinline__ int lin_index(const int32_t* idx, int total, int r, i
     return -1;
 }
 
-template <int ACT>
-__device__ __forceinline__ void lin_act16(float (&v)[16], const float (&u)[16]) {
+template <int ACT, int N>
+__device__ __forceinline__ void lin_act_all(float (&v)[N], const float (&u)[N]) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = lin_act(ACT, v[j], u[j]);
+    for (int j = 0; j < N; ++j) v[j] = lin_act(ACT, v[j], u[j]);
 }
 
 }  // namespace moe

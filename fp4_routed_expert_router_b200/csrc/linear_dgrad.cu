@@ -1,0 +1,12 @@
+// linear_dgrad.cu -- the tensor-core kernels of dx = dz w (+ dz_up w_up).
+#include "linear_tc.cuh"
+
+namespace moe {
+
+cudaError_t lin_launch_dgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
+    return lt_launch<LIN_DGRAD, false>(a, p, m, tma, s);
+}
+
+cudaError_t lin_allow_dgrad(int bytes) { return lt_allow<LIN_DGRAD, false>(bytes); }
+
+}  // namespace moe

@@ -2,32 +2,48 @@
 // (tcgen05 + TMEM), dense and grouped by expert.
 //
 // out[row][c] = sum_q A(q, c) B(q, row) (linear_common.cuh).  c, the contiguous
-// index of the output, is the M side of tcgen05.mma: 128 TMEM lanes; the rows
-// are its N side, BN <= 256 columns.  A warp of the epilogue therefore holds
-// 32 neighbouring c of a row in its lanes and writes them straight to memory,
-// with bias and activation per lane, and a handful of rows (decode) costs an
-// MMA of N = 16 instead of a 128-row tile that is mostly empty.
+// index of the output, is the M side of tcgen05.mma: 128 TMEM lanes a CTA; the
+// rows are its N side, BN <= 256 columns.  A warp of the epilogue therefore
+// holds 32 neighbouring c of a row in its lanes and writes them straight to
+// memory, with bias and activation per lane, and a handful of rows (decode)
+// costs an MMA of N = 16 instead of a 128-row tile that is mostly empty.
 //
 // Operands in shared memory, 64 terms (q) a stage, 128-byte swizzle:
 //   forward  A = w    K-major  (row c, 64 q)       B = x   K-major  (row, 64 q)
 //   dgrad    A = w    MN-major (row q, 64 c) x 2   B = dz  K-major
 //   wgrad    A = x    MN-major (row q, 64 c) x 2   B = dz  MN-major (row q, 64 rows) x BN / 64
 // Both majors are read by the tensor core as they lie in memory, so nothing is
-// transposed anywhere.  SwiGLU's forward keeps two accumulators (w, w_up) fed
-// by one B; its dgrad runs on through a second pair (dz_up, w_up).
+// transposed anywhere.  SwiGLU's forward gives a tile 64 c: lanes 32 g + l hold
+// w row 16 g + l (l < 16) or w_up row 16 g + l - 16, so gate and up of a value
+// meet in one shuffle and the tile keeps its N = 256; SwiGLU's dgrad runs on
+// through a second operand pair (dz_up, w_up).
+//
+// Three shapes of a tile, chosen by lt_plan's cost estimate:
+//   pair   (CG = 2) two CTAs of a cluster form one MMA (cta_group::2): 256 c x BN rows,
+//          each CTA loads its 128 c and half of the rows.  At 256 x 256 an SM
+//          reads 64 bytes from L2 per MMA cycle instead of 96 for 128 x 256,
+//          which is what bounds a single CTA's tile here (~11 TB/s measured).
+//   single one CTA, 128 c x BN rows.
+//   split  a cluster of S CTAs shares one tile's sum when there are fewer tiles
+//          than SMs: each sums its part of q, the fp32 parts meet in shared
+//          memory (DSMEM reads in rank order, so the result does not depend on
+//          timing) and each CTA finishes its share of the rows.
 //
 // Groups: rows of a tile belong to one group; a tile that ends inside a group's
 // last rows reads what lies behind them into columns that are not stored.  In
 // wgrad the group is the sum: its last stage runs only the 16-term steps it
-// needs, and the up to 15 foreign rows in the last step are zeroed in both
-// operands first (0 * inf would not be 0).
+// needs and is copied by the gather warps, which put zeros behind the group's
+// last row in both operands (a foreign row times zero could still be NaN).
 //
-// One persistent CTA per SM.  Warps: 0 loads (TMA; with x_rows one
-// tile::gather4 per four rows and lane), 1 issues the MMAs, 4-11 epilogue
-// (TMEM lane group warp % 4, 16-column units shared by two warps), 12-15 (only
-// for operands TMA cannot take: a base that is not 16-byte aligned or rows
-// that are not multiples of 8 values) load element by element.  Two
+// Persistent CTAs, one per SM.  Warps: 0 TMA loads, 1 issues the MMAs, 2-3 copy
+// gathered rows (x_rows) and ragged ends with 16-byte cp.async -- one tile::gather4 per four rows
+// and 64 values ran at 6 bytes a cycle, a quarter of the speed needed -- 4-11
+// epilogue (TMEM lane group warp % 4, 16-column units shared by two warps), 12-15
+// (only for operands TMA cannot take: a base that is not 16-byte aligned or
+// rows that are not multiples of 8 values) load element by element.  Two
 // accumulators, so the epilogue of a tile overlaps the next one's products.
+// fp32 outputs: the tensor core cuts its sums (measured 1e-9 relative per term,
+// always towards zero), so spans of 640 terms are added up in registers.
 // Every wait is bounded; the first that gives up ends the CTA's other waits
 // and latches ETIMEOUT, after the copies in flight have landed.
 #pragma once
@@ -35,28 +51,33 @@
 #include <cudaTypedefs.h>
 
 #include "linear_common.cuh"
-#include "tc_prefill.cuh"
 #include "tma.cuh"
+#include "umma.cuh"
 
 namespace moe {
 
-constexpr int kLtM = 128;            // c of a tile (TMEM lanes)
+constexpr int kLtM = 128;            // TMEM lanes of a CTA: A rows of its tile
 constexpr int kLtBK = 64;            // terms per stage: one 128-byte swizzle row
 constexpr int kLtATile = kLtM * 128; // bytes of one A tile of a stage
 constexpr int kLtEpiWarps = 8;
 constexpr int kLtMaxStages = 12;
 constexpr int kLtPromote = 10;       // fp32 outputs: stages summed in the tensor core before the sum moves to registers
 constexpr int kLtRaster = 8;         // row tiles walked together, so that operands of neighbouring tiles meet in L2
+constexpr int kLtOffIdx = 256;       // shared memory: barriers, source rows of the gather (256), tile prefix
+constexpr int kLtOffPrefix = kLtOffIdx + 256 * 4;
 __host__ __device__ constexpr int lt_threads(bool tma) { return (4 + kLtEpiWarps + (tma ? 0 : 4)) * 32; }
 
 struct LtPlan {
     int bn;         // output rows of a tile
+    int cg;         // CTAs of one MMA (1 or 2)
+    int split;      // CTAs that share a tile's sum (cg = 1)
+    int ct;         // c of one CTA's tile (128, SwiGLU forward 64)
     int bbox;       // rows of one K-major B box
-    int stages, stage_bytes, off_ring, smem;
+    int stages, stage_bytes, off_ring, off_red, smem;
     int n_ct;       // tiles along c
     int promote;    // stages per accumulation span (0: the whole sum)
     int tmem_cols;
-    int grid;
+    int grid;       // CTAs
 };
 
 struct LtMaps {
@@ -72,59 +93,178 @@ __device__ __forceinline__ uint64_t lt_desc_mn(uint32_t smem_addr) {
 
 // D fp32 (bits 4-5), operand type in bits 7-9 and 10-12 (0 f16, 1 bf16), bit 15 / 16: A / B is MN-major,
 // N >> 3 at bits 17-22, M >> 4 at bits 24-28.
-__device__ __forceinline__ uint32_t lt_idesc(int type, bool a_mn, bool b_mn, int n) {
+__device__ __forceinline__ uint32_t lt_idesc(int type, bool a_mn, bool b_mn, int m, int n) {
     const uint32_t t = type == LIN_BF16 ? 1u : 0u;
     return (1u << 4) | (t << 7) | (t << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
-           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kLtM >> 4) << 24);
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+template <int CG>
 __device__ __forceinline__ void lt_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
-        : "memory");
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+            : "memory");
 }
 
-__device__ __forceinline__ void lt_tma3(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-            "r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-        : "memory");
+// Signal `bar` (in both CTAs of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void lt_commit(uint64_t* bar) {
+    if constexpr (CG == 1)
+        umma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
 }
 
-// Four rows (any rows) x 64 values; the map's box is one row high.
-__device__ __forceinline__ void lt_gather4(void* dst, const CUtensorMap* map, int c0, int4 r, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_u32(bar))
-        : "memory");
+__device__ __forceinline__ uint32_t lt_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
+
+// Address of this CTA's shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t lt_map(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void lt_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void lt_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Bounded wait for phase `parity` of `bar` that also orders what other CTAs of the cluster wrote before they
+// arrived.  The probes come without a pause (SLEEP = 0, the two warps whose pace sets the kernel's) or SLEEP ns apart;
+// the timer, whose reading costs about as much as a stage, is looked at every 256 probes only.
+template <int SLEEP>
+__device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
+    const uint32_t at = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(at), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (SLEEP) __nanosleep(SLEEP);
+        if ((n & 255) == 0) {
+            if (*abort) return false;
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > timeout_ns) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float lt_ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void lt_cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+// 3-d tile of 64 inner values into this CTA's shared memory; `bar` may be the barrier of the pair's first CTA.
+template <int CG>
+__device__ __forceinline__ void lt_tma3(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
+}
+
+// 16 bytes, of which the last 16 - n are zeros.
+__device__ __forceinline__ void lt_cp16(uint8_t* dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+
+// One lane of a converged warp.  The compiler then knows that a single thread issues TMA and MMA instructions; behind
+// a plain lane test it serialises each of them over the warp (75 cycles apiece, measured).
+__device__ __forceinline__ bool lt_elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// Place in the ring of stages: slot and the parity of its current use.
+struct LtRing {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int S) {
+        if (++st == S) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+};
 
 struct LtTile {
     int e, which;   // group, output (wgrad: dw or dw_up)
-    int c0;         // first c
+    int c0;         // first c of this CTA
     int r0, nrows;  // first output row (forward, dgrad: grouped row; wgrad: row of the group's output), rows
     int p0, nq;     // wgrad: the group's first row and row count
-    int nkb;        // stages
+    int kb0, kb1;   // this CTA's stages of the sum
+    int n;          // N of the MMA
+    int b0;         // first B row of this CTA, from r0
+    int nb;         // B rows of this CTA's stage
 };
 
-template <int KIND, bool DUAL, bool TMA>
+template <int KIND, bool DUAL, bool TMA, int CG>
 __global__ void __launch_bounds__(lt_threads(TMA), 1)
 lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps maps) {
     constexpr bool WG = KIND == LIN_WGRAD;
     constexpr bool A_MN = KIND != LIN_FWD;
-    constexpr int NACC = DUAL ? 2 : 1;
     extern __shared__ __align__(1024) uint8_t lt_smem_raw[];
     uint8_t* smem = lt_smem_raw + ((1024u - (smem_u32(lt_smem_raw) & 1023u)) & 1023u);
     const int S = p.stages, BN = p.bn;
+    static_assert(TMA || CG == 1);
+    constexpr int cg = CG;
+    const int split = CG == 1 ? p.split : 1;
+    const int csize = cg * split;                          // CTAs of a cluster (one of the two is 1)
+    const int rank = csize > 1 ? static_cast<int>(lt_rank()) : 0;
+    const bool gathers = a.gather != nullptr && KIND != LIN_DGRAD && TMA;
+    const bool copies = gathers || (WG && TMA && a.offsets != nullptr);   // warps 2-3 take part in every stage
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + kLtMaxStages;
     uint64_t* acc_full = empty + kLtMaxStages;
     uint64_t* acc_empty = acc_full + 2;
-    int* tprefix = reinterpret_cast<int*>(smem + 512);   // [E+1] tiles before group e (forward, dgrad)
+    uint64_t* red_full = acc_empty + 2;                    // every part of a split tile is in shared memory
+    uint64_t* red_empty = red_full + 1;                    // and has been read
+    int* src_row = reinterpret_cast<int*>(smem + kLtOffIdx);
+    int* tprefix = reinterpret_cast<int*>(smem + kLtOffPrefix);   // [E+1] tiles before group e (forward, dgrad)
+    float* red = reinterpret_cast<float*>(smem + p.off_red);      // [BN][128] this CTA's part (split)
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     volatile int* abort_flag = &abort_s;
@@ -132,19 +272,29 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], TMA ? 1 : 4);
+            mbar_init(&full[s], TMA ? 1 + (copies ? 2 * cg : 0) : 4);
             mbar_init(&empty[s], 1);
         }
         for (int q = 0; q < 2; ++q) {
             mbar_init(&acc_full[q], 1);
-            mbar_init(&acc_empty[q], kLtEpiWarps);
+            mbar_init(&acc_empty[q], kLtEpiWarps * cg);
         }
+        mbar_init(red_full, kLtEpiWarps * split);
+        mbar_init(red_empty, kLtEpiWarps * split);
         abort_s = 0;
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_s)),
-                     "r"(static_cast<uint32_t>(p.tmem_cols)));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&tmem_base_s)),
+                         "r"(static_cast<uint32_t>(p.tmem_cols)));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(&tmem_base_s)),
+                         "r"(static_cast<uint32_t>(p.tmem_cols)));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        }
     }
     pdl_wait();
     if (!WG && warp == 0) {   // tiles before each group
@@ -168,16 +318,17 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     if (tid == 0) fence_barrier_init();
     tc_fence_before();
     __syncthreads();
+    if (csize > 1) lt_cluster_sync();   // the others' barriers exist before anything signals them
     tc_fence_after();
     pdl_trigger();
     const uint32_t tmem = tmem_base_s;
     const int n_rt_w = WG ? (a.out_n + BN - 1) / BN : 0;
     const int n_work = WG ? p.n_ct * n_rt_w * a.E * (a.b[1] ? 2 : 1) : tprefix[a.E];
-    const int G = gridDim.x;
+    const int w0 = blockIdx.x / csize, G = gridDim.x / csize;
 
     // Tile w of the walk; false when its group is not sound (nothing is computed or written).
     auto tile_of = [&](int w, LtTile& t) -> bool {
-        int v, n_rt;
+        int v, n_rt, nkb;
         t.which = 0;
         if (WG) {
             const int per = p.n_ct * n_rt_w;
@@ -189,7 +340,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             int p1;
             if (!lin_group(a.offsets, a.rows, t.e, a.err, &t.p0, &p1)) return false;
             t.nq = p1 - t.p0;
-            t.nkb = (t.nq + kLtBK - 1) / kLtBK;
+            nkb = (t.nq + kLtBK - 1) / kLtBK;
         } else {
             int lo = 0, hi = a.E - 1;   // the last group that starts at or before w (empty groups start where they end)
             while (lo < hi) {
@@ -201,12 +352,12 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             n_rt = (tprefix[lo + 1] - tprefix[lo]) / p.n_ct;
             t.p0 = 0;
             t.nq = a.Q;
-            t.nkb = (a.Q + kLtBK - 1) / kLtBK * (KIND == LIN_DGRAD && a.b[1] ? 2 : 1);
+            nkb = (a.Q + kLtBK - 1) / kLtBK * (KIND == LIN_DGRAD && a.b[1] ? 2 : 1);
         }
         const int blk = v / (kLtRaster * p.n_ct);
         v -= blk * kLtRaster * p.n_ct;
         const int in_blk = min(kLtRaster, n_rt - blk * kLtRaster);
-        t.c0 = v / in_blk * kLtM;
+        t.c0 = (v / in_blk * cg + (cg == 2 ? rank : 0)) * p.ct;
         const int rt = blk * kLtRaster + v % in_blk;
         if (WG) {
             t.r0 = rt * BN;
@@ -220,117 +371,208 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             t.r0 = p0 + rt * BN;
             t.nrows = min(BN, p1 - t.r0);
         }
+        const int step = 16 * cg;
+        t.n = (t.nrows + step - 1) / step * step;
+        t.b0 = cg == 2 ? rank * (t.n / 2) : 0;
+        t.nb = t.n / cg;
+        t.kb0 = 0;
+        t.kb1 = nkb;
+        if (split > 1) {
+            t.kb0 = static_cast<int>(static_cast<long long>(nkb) * rank / split);
+            t.kb1 = static_cast<int>(static_cast<long long>(nkb) * (rank + 1) / split);
+        }
         return true;
     };
     auto stage_a = [&](int st) { return smem + p.off_ring + static_cast<size_t>(st) * p.stage_bytes; };
-    auto stage_b = [&](int st) { return stage_a(st) + NACC * kLtATile; };
+    auto stage_b = [&](int st) { return stage_a(st) + kLtATile; };
     const int half_kb = (a.Q + kLtBK - 1) / kLtBK;   // dgrad: stages of the first pair
-
+    const uint32_t ring0 = smem_u32(smem + p.off_ring);
     if (TMA && warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        int g = 0;
-        bool stop = false;
-        for (int w = blockIdx.x; w < n_work && !stop; w += G) {
-            LtTile t;
-            if (!tile_of(w, t)) continue;
-            const int nbox = WG ? (t.nrows + 63) / 64 : (t.nrows + p.bbox - 1) / p.bbox;
-            const int nquad = (t.nrows + 3) / 4;
-            const bool gather = a.gather != nullptr && KIND != LIN_DGRAD;
-            const uint32_t bytes =
-                static_cast<uint32_t>(NACC * kLtATile + (WG ? nbox * 8192 : gather ? nquad * 512 : nbox * p.bbox * 128));
-            int4 idx[2];
-            if (KIND == LIN_FWD && gather) {   // rows 4 lane .. and 128 + 4 lane .. of the tile (clamped; not stored)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    int* ip = reinterpret_cast<int*>(&idx[h]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = t.r0 + min(t.nrows - 1, 128 * h + 4 * lane + j);
-                        const int v = __ldg(a.gather + r);
-                        ip[j] = v >= 0 && v < a.gather_total ? v : 0;
+        if (lt_elect()) {
+            LtRing ring;
+            int g = 0;
+            bool stop = false;
+            const uint32_t bar0 = cg == 2 ? lt_map(full, 0) : smem_u32(full);
+            // this CTA's B boxes: rows b0 .. b0 + nb, none behind the tile's last row
+            const int bstep = WG ? 64 : p.bbox, box_b = bstep * 128;
+            const bool a_tma = !(gathers && WG), b_tma = !(gathers && !WG);
+            for (int w = w0; w < n_work && !stop; w += G) {
+                LtTile t;
+                if (!tile_of(w, t)) continue;
+                const int nbox = (t.nb + bstep - 1) / bstep;
+                const uint32_t all =
+                    static_cast<uint32_t>(cg * ((a_tma ? kLtATile : 0) + (b_tma ? nbox * box_b : 0)));
+                const int br = t.r0 + t.b0;
+                for (int kb = t.kb0; kb < t.kb1; ++kb, ++g, ring.next(S)) {
+                    if (!lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, a.timeout_ns)) {
+                        latch_error(a.err, ERR_ETIMEOUT, g, KID_LINEAR);
+                        stop = true;
+                        break;
                     }
-                }
-            }
-            for (int kb = 0; kb < t.nkb; ++kb, ++g) {
-                const int st = g % S;
-                int ok = 1;
-                if (g >= S && lane == 0) ok = mbar_poll(&empty[st], ((g / S) - 1) & 1, abort_flag, a.timeout_ns);
-                if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
-                    if (lane == 0) latch_error(a.err, ERR_ETIMEOUT, g, KID_LINEAR);
-                    stop = true;
-                    break;
-                }
-                uint8_t* sa = stage_a(st);
-                uint8_t* sb = stage_b(st);
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[st], bytes);
+                    const uint32_t sa = ring0 + ring.st * p.stage_bytes, sb = sa + kLtATile;
+                    const uint32_t bar = bar0 + ring.st * 8;
+                    const bool ragged = WG && copies && t.nq - kb * kLtBK < kLtBK;   // warps 2-3 copy all of it
+                    if (cg == 1 || rank == 0)                                        // both CTAs' bytes
+                        mbar_arrive_expect_tx(&full[ring.st], ragged ? 0u : all);
                     if (KIND == LIN_FWD) {
-                        lt_tma3(sa, &maps.a0, kb * kLtBK, t.c0, t.e, &full[st]);
-                        if (DUAL) lt_tma3(sa + kLtATile, &maps.a1, kb * kLtBK, t.c0, t.e, &full[st]);
-                        if (!gather)
+                        if (DUAL) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                lt_tma3<CG>(sa + i * 4096, &maps.a0, kb * kLtBK, t.c0 + 16 * i, t.e, bar);
+                                lt_tma3<CG>(sa + i * 4096 + 2048, &maps.a1, kb * kLtBK, t.c0 + 16 * i, t.e, bar);
+                            }
+                        } else {
+                            lt_tma3<CG>(sa, &maps.a0, kb * kLtBK, t.c0, t.e, bar);
+                        }
+                        if (b_tma)
                             for (int b = 0; b < nbox; ++b)
-                                lt_tma3(sb + b * p.bbox * 128, &maps.b0, kb * kLtBK, t.r0 + b * p.bbox, 0, &full[st]);
+                                lt_tma3<CG>(sb + b * box_b, &maps.b0, kb * kLtBK, br + b * bstep, 0, bar);
                     } else if (KIND == LIN_DGRAD) {
                         const bool second = kb >= half_kb;
                         const int q = (second ? kb - half_kb : kb) * kLtBK;
                         const CUtensorMap* ma = second ? &maps.a1 : &maps.a0;
                         const CUtensorMap* mb = second ? &maps.b1 : &maps.b0;
-                        lt_tma3(sa, ma, t.c0, q, t.e, &full[st]);
-                        lt_tma3(sa + 8192, ma, t.c0 + 64, q, t.e, &full[st]);
-                        for (int b = 0; b < nbox; ++b)
-                            lt_tma3(sb + b * p.bbox * 128, mb, q, t.r0 + b * p.bbox, 0, &full[st]);
-                    } else {
+                        lt_tma3<CG>(sa, ma, t.c0, q, t.e, bar);
+                        lt_tma3<CG>(sa + 8192, ma, t.c0 + 64, q, t.e, bar);
+                        for (int b = 0; b < nbox; ++b) lt_tma3<CG>(sb + b * box_b, mb, q, br + b * bstep, 0, bar);
+                    } else if (!ragged) {
                         const CUtensorMap* mb = t.which ? &maps.b1 : &maps.b0;
-                        if (!gather) {
-                            lt_tma3(sa, &maps.a0, t.c0, t.p0 + kb * kLtBK, 0, &full[st]);
-                            lt_tma3(sa + 8192, &maps.a0, t.c0 + 64, t.p0 + kb * kLtBK, 0, &full[st]);
+                        if (a_tma) {
+                            lt_tma3<CG>(sa, &maps.a0, t.c0, t.p0 + kb * kLtBK, 0, bar);
+                            lt_tma3<CG>(sa + 8192, &maps.a0, t.c0 + 64, t.p0 + kb * kLtBK, 0, bar);
                         }
                         for (int b = 0; b < nbox; ++b)
-                            lt_tma3(sb + b * 8192, mb, t.r0 + b * 64, t.p0 + kb * kLtBK, 0, &full[st]);
+                            lt_tma3<CG>(sb + b * box_b, mb, br + b * bstep, t.p0 + kb * kLtBK, 0, bar);
                     }
                 }
-                __syncwarp();
-                if (gather && KIND == LIN_FWD) {
-                    if (lane < nquad) lt_gather4(sb + lane * 512, &maps.b0, kb * kLtBK, idx[0], &full[st]);
-                    if (lane + 32 < nquad) lt_gather4(sb + (lane + 32) * 512, &maps.b0, kb * kLtBK, idx[1], &full[st]);
-                } else if (gather && WG) {   // 16 quads of q rows x 2 blocks of 64 c: one per lane
-                    int4 r;
-                    int* ip = reinterpret_cast<int*>(&r);
-                    const int quad = lane & 15, blk = lane >> 4;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int v = __ldg(a.gather + t.p0 + min(t.nq - 1, kb * kLtBK + 4 * quad + j));
-                        const bool in = v >= 0 && v < a.gather_total;
-                        if (!in) latch_error(a.err, ERR_EINVAL, v, KID_LINEAR);
-                        ip[j] = in ? v : 0;
-                    }
-                    lt_gather4(sa + blk * 8192 + quad * 512, &maps.a0, t.c0 + 64 * blk, r, &full[st]);
+            }
+            if (*abort_flag && (cg == 1 || rank == 0)) {   // copies still in flight land before the CTA may exit
+                volatile int fresh = 0;                    // (a pair's second CTA waits for the first)
+                for (int st = 0; st < S && st < g; ++st) {
+                    const int last = st + ((g - 1 - st) / S) * S;
+                    fresh = 0;
+                    mbar_wait(&full[st], (last / S) & 1, &fresh);
                 }
-                __syncwarp();
             }
         }
-        if (*abort_flag && lane == 0) {   // copies still in flight land before the CTA may exit
-            volatile int fresh = 0;
-            for (int st = 0; st < S && st < g; ++st) {
-                const int last = st + ((g - 1 - st) / S) * S;
-                fresh = 0;
-                mbar_wait(&full[st], (last / S) & 1, &fresh);
+    } else if (copies && (warp == 2 || warp == 3)) {
+        // ------------------------------------------------------------ gathered rows and ragged ends (64 threads)
+        // forward: the tile's B rows, 8 chunks of 16 bytes each; wgrad: the stage's 64 A rows (2 x 8 chunks) and, in a
+        // group's last stage, its B rows too.  A stage is handed over once its copies have landed, `lag` stages later.
+        const int lt = tid - 64;
+        const uint16_t* xb = static_cast<const uint16_t*>(WG ? a.a[0] : a.b[0]);
+        const long long ldx = WG ? a.lda : a.ldb;
+        const uint32_t bar0 = cg == 2 ? lt_map(full, 0) : lt_map(full, static_cast<uint32_t>(rank));
+        const int lag = S >= 6 ? 3 : 1;
+        LtRing ring, out;
+        int g = 0, given = 0;
+        bool stop = false;
+        auto source = [&](int r) {   // row of x behind grouped row r, -1: counts as zero
+            if (!a.gather) return r;
+            const int v = __ldg(a.gather + r);
+            if (v >= 0 && v < a.gather_total) return v;
+            latch_error(a.err, ERR_EINVAL, r, KID_LINEAR);
+            return -1;
+        };
+        auto slot_free = [&](const LtRing& at) {   // (warp-uniform)
+            int ok = 1;
+            if (lane == 0) {
+                ok = lt_poll<0>(&empty[at.st], at.ph ^ 1, abort_flag, a.timeout_ns);
+                if (!ok) latch_error(a.err, ERR_ETIMEOUT, g, KID_LINEAR);
+            }
+            return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+        };
+        auto both = [&](bool ok) {   // meet the other warp; whether both are fine
+            uint32_t r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                "barrier.cta.red.and.aligned.pred q, 1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                : "=r"(r)
+                : "r"(ok ? 1u : 0u)
+                : "memory");
+            return r != 0;
+        };
+        auto give = [&]() {          // the oldest stage not yet handed over has landed
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) lt_arrive_remote(bar0 + out.st * 8);
+            out.next(S);
+            ++given;
+        };
+        auto copy = [&](uint8_t* tile, int row, int ch, const uint16_t* base, long long ld, int r, int col, int width) {
+            const int n = r < 0 ? 0 : max(0, min(16, (width - col) * 2));
+            lt_cp16(tile + row * 128 + ((ch ^ (row & 7)) << 4),
+                    n == 0 ? base : base + static_cast<size_t>(r) * ld + col, n);
+        };
+        for (int w = w0; w < n_work && !stop; w += G) {
+            LtTile t;
+            if (!tile_of(w, t)) continue;
+            if (!WG) {
+                asm volatile("bar.sync 1, 64;" ::: "memory");
+                for (int i = lt; i < t.nb; i += 64) {
+                    const int r = t.b0 + i;
+                    src_row[i] = r < t.nrows ? source(t.r0 + r) : -1;
+                }
+                asm volatile("bar.sync 1, 64;" ::: "memory");
+            }
+            for (int kb = t.kb0; kb < t.kb1; ++kb, ++g, ring.next(S)) {
+                const int st = ring.st;
+                const int valid = t.nq - kb * kLtBK;
+                const bool ragged = WG && valid < kLtBK;
+                const bool mine = gathers || ragged;
+                // two tables in turn: the other one may still be read
+                if (WG && mine) src_row[(g & 1) * 64 + lt] = lt < valid ? source(t.p0 + kb * kLtBK + lt) : -1;
+                if (!both(slot_free(ring))) {
+                    stop = true;
+                    break;
+                }
+                if (mine && !WG) {
+                    for (int i = lt >> 3; i < t.nb; i += 8)
+                        copy(stage_b(st), i, lt & 7, xb, ldx, src_row[i], kb * kLtBK + (lt & 7) * 8, a.Q);
+                } else if (mine) {
+                    const int rows = ragged ? (valid + 15) / 16 * 16 : kLtBK;
+                    const int ch = lt & 15;
+#pragma unroll 4
+                    for (int i = lt >> 4; i < rows; i += 4)
+                        copy(stage_a(st) + (ch >> 3) * 8192, i, ch & 7, xb, ldx, src_row[(g & 1) * 64 + i],
+                             t.c0 + ch * 8, a.C);
+                    if (ragged) {
+                        const uint16_t* bb = static_cast<const uint16_t*>(a.b[t.which]);
+                        const int nch = (t.nb + 63) / 64 * 8;
+                        for (int i = lt; i < rows * nch; i += 64) {
+                            const int row = i / nch, c = i - row * nch;
+                            copy(stage_b(st) + (c >> 3) * 8192, row, c & 7, bb, a.ldb,
+                                 row < valid ? t.p0 + kb * kLtBK + row : -1, t.r0 + t.b0 + c * 8, a.out_n);
+                        }
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (!gathers && !ragged) {
+                    while (given <= g) give();   // nothing of this stage is in flight here
+                } else if (g - given >= lag) {
+                    if (lag == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+                    else asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    give();
+                }
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        while (given < g) give();
     } else if (!TMA && warp >= 4 + kLtEpiWarps) {
         // ------------------------------------------------------------ element loader (128 threads)
         const int lt = tid - (4 + kLtEpiWarps) * 32;
-        int g = 0;
+        LtRing ring;
         bool stop = false;
-        for (int w = blockIdx.x; w < n_work && !stop; w += G) {
+        for (int w = w0; w < n_work && !stop; w += G) {
             LtTile t;
             if (!tile_of(w, t)) continue;
-            for (int kb = 0; kb < t.nkb; ++kb, ++g) {
-                const int st = g % S;
+            for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next(S)) {
+                const int st = ring.st;
                 int ok = 1;
-                if (g >= S && lane == 0) ok = mbar_poll(&empty[st], ((g / S) - 1) & 1, abort_flag, a.timeout_ns);
+                if (lane == 0) ok = lt_poll<0>(&empty[st], ring.ph ^ 1, abort_flag, a.timeout_ns);
                 if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
-                    if (lane == 0) latch_error(a.err, ERR_ETIMEOUT, g, KID_LINEAR);
+                    if (lane == 0) latch_error(a.err, ERR_ETIMEOUT, kb, KID_LINEAR);
                     stop = true;
                     break;
                 }
@@ -352,14 +594,15 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 uint8_t* sa = stage_a(st);
                 uint8_t* sb = stage_b(st);
                 if (KIND == LIN_FWD) {
-                    for (int m = 0; m < NACC; ++m) {
-                        const uint16_t* base = static_cast<const uint16_t*>(a.a[m]) +
-                                               static_cast<size_t>(t.e) * a.a_gstride + q0;
-                        fill(sa + m * kLtATile, kLtM,
-                             [&](int sr) -> const uint16_t* {
-                                 return t.c0 + sr < a.C ? base + static_cast<size_t>(t.c0 + sr) * a.lda : nullptr;
-                             }, nq);
-                    }
+                    const size_t at = static_cast<size_t>(t.e) * a.a_gstride + q0;
+                    const uint16_t* w0p = static_cast<const uint16_t*>(a.a[0]) + at;
+                    const uint16_t* w1p = static_cast<const uint16_t*>(a.a[1]) + at;
+                    fill(sa, kLtM,
+                         [&](int sr) -> const uint16_t* {
+                             const int c = t.c0 + (DUAL ? (sr >> 5) * 16 + (sr & 15) : sr);
+                             const uint16_t* base = DUAL && (sr & 16) ? w1p : w0p;
+                             return c < a.C ? base + static_cast<size_t>(c) * a.lda : nullptr;
+                         }, nq);
                 } else {
                     const uint16_t* base = static_cast<const uint16_t*>(a.a[second ? 1 : 0]) +
                                            (WG ? 0 : static_cast<size_t>(t.e) * a.a_gstride);
@@ -386,10 +629,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     fill(sb, t.nrows,
                          [&](int sr) -> const uint16_t* {
                              int row = t.r0 + sr;
-                             if (KIND == LIN_FWD && a.gather) {
-                                 const int v = __ldg(a.gather + row);
-                                 row = v >= 0 && v < a.gather_total ? v : -1;
-                             }
+                             if (KIND == LIN_FWD) row = lin_index(a.gather, a.gather_total, row, a.err);
                              return row < 0 ? nullptr : bb + static_cast<size_t>(row) * a.ldb + q0;
                          }, nq);
                 }
@@ -398,141 +638,131 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 if (lane == 0) mbar_arrive(&full[st]);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 && (cg == 1 || rank == 0)) {
         // ------------------------------------------------------------ MMA issuer
-        int g = 0, acc = 0;
-        for (int w = blockIdx.x; w < n_work; w += G) {
-            LtTile t;
-            if (!tile_of(w, t)) continue;
-            const int n = (t.nrows + 15) / 16 * 16;
-            const uint32_t idesc = lt_idesc(a.type, A_MN, WG, n);
-            const int span = p.promote ? p.promote : t.nkb;
-            for (int k0 = 0; k0 < t.nkb; k0 += span, ++acc) {
-                const int ab = acc & 1;
-                if (acc >= 2 && !mbar_poll(&acc_empty[ab], ((acc >> 1) - 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
-                    latch_error(a.err, ERR_ETIMEOUT, acc, KID_LINEAR);
-                tc_fence_after();
-                const uint32_t d = tmem + ab * (NACC * BN);
-                const int k1 = min(t.nkb, k0 + span);
-                for (int kb = k0; kb < k1; ++kb, ++g) {
-                    const int st = g % S;
-                    if (!mbar_poll(&full[st], (g / S) & 1, abort_flag, a.timeout_ns) && lane == 0)
-                        latch_error(a.err, ERR_ETIMEOUT, g, KID_LINEAR);
-                    int steps = kLtBK / 16;
-                    if (WG) {
-                        const int valid = t.nq - kb * kLtBK;
-                        if (valid < kLtBK) {   // the group's last stage
-                            steps = (valid + 15) / 16;
-                            if (TMA && (valid & 15)) {   // foreign rows of the last step, in every 64-wide block
-                                const int nz = steps * 16 - valid, blocks = 2 + (t.nrows + 63) / 64;
-                                uint8_t* base = stage_a(st) + valid * 128;
-                                for (int i = lane; i < blocks * nz * 8; i += 32)
-                                    *reinterpret_cast<uint4*>(base + (i / (nz * 8)) * 8192 + (i % (nz * 8)) * 16) =
-                                        make_uint4(0, 0, 0, 0);
-                                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                                __syncwarp();
-                            }
-                        }
-                    }
+        if (lt_elect()) {
+            LtRing ring;
+            int acc = 0;
+            const uint64_t ad0 = A_MN ? lt_desc_mn(ring0) : umma_desc_sw128(ring0);
+            const uint64_t bd0 = WG ? lt_desc_mn(ring0 + kLtATile) : umma_desc_sw128(ring0 + kLtATile);
+            for (int w = w0; w < n_work; w += G) {
+                LtTile t;
+                if (!tile_of(w, t)) continue;
+                const uint32_t idesc = lt_idesc(a.type, A_MN, WG, kLtM * cg, t.n);
+                const int span = p.promote ? p.promote : t.kb1 - t.kb0;
+                for (int k0 = t.kb0; k0 < t.kb1; k0 += span, ++acc) {
+                    const int ab = acc & 1;
+                    if (!lt_poll<0>(&acc_empty[ab], ((acc >> 1) & 1) ^ 1, abort_flag, a.timeout_ns))
+                        latch_error(a.err, ERR_ETIMEOUT, acc, KID_LINEAR);
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t sa = smem_u32(stage_a(st)), sb = smem_u32(stage_b(st));
-                        const uint64_t ad = A_MN ? lt_desc_mn(sa) : umma_desc_sw128(sa);
-                        const uint64_t bd = WG ? lt_desc_mn(sb) : umma_desc_sw128(sb);
-                        for (int k = 0; k < steps; ++k) {   // 16 terms: 32 bytes of a K-major row, 16 rows of MN-major
-                            const uint64_t ak = ad + static_cast<uint64_t>(A_MN ? 128 * k : 2 * k);
-                            const uint64_t bk = bd + static_cast<uint64_t>(WG ? 128 * k : 2 * k);
-                            const uint32_t on = kb > k0 || k > 0 ? 1u : 0u;
-                            lt_mma(d, ak, bk, idesc, on);
-                            if (DUAL) lt_mma(d + BN, ak + (kLtATile >> 4), bk, idesc, on);
-                        }
-                        umma_commit(&empty[st]);
+                    const uint32_t d = tmem + ab * BN;
+                    const int k1 = min(t.kb1, k0 + span);
+                    for (int kb = k0; kb < k1; ++kb, ring.next(S)) {
+                        if (!lt_poll<0>(&full[ring.st], ring.ph, abort_flag, a.timeout_ns))
+                            latch_error(a.err, ERR_ETIMEOUT, kb, KID_LINEAR);
+                        tc_fence_after();
+                        const uint64_t off = static_cast<uint64_t>(ring.st * (p.stage_bytes >> 4));
+                        int steps = kLtBK / 16;   // the group's last stage may have fewer
+                        if (WG) steps = min(steps, (t.nq - kb * kLtBK + 15) / 16);
+#pragma unroll
+                        for (int k = 0; k < kLtBK / 16; ++k)   // 32 bytes of a K-major row, 16 rows of MN-major
+                            if (!WG || k < steps)
+                                lt_mma<CG>(d, ad0 + off + (A_MN ? 128 * k : 2 * k), bd0 + off + (WG ? 128 * k : 2 * k),
+                                           idesc, kb > k0 || k > 0 ? 1u : 0u);
+                        lt_commit<CG>(&empty[ring.st]);
                     }
-                    __syncwarp();
+                    lt_commit<CG>(&acc_full[ab]);
                 }
-                if (lane == 0) umma_commit(&acc_full[ab]);
-                __syncwarp();
             }
+            for (int k = 1; k <= 2; ++k)   // the last commits land before TMEM is released
+                if (acc >= k) {
+                    volatile int fresh = 0;
+                    mbar_wait(&acc_full[(acc - k) & 1], ((acc - k) >> 1) & 1, &fresh);
+                }
         }
-        for (int k = 1; k <= 2; ++k)   // the last commits land before TMEM is released
-            if (acc >= k && lane == 0) {
-                volatile int fresh = 0;
-                mbar_wait(&acc_full[(acc - k) & 1], ((acc - k) >> 1) & 1, &fresh);
-            }
     } else if (warp >= 4 && warp < 4 + kLtEpiWarps) {
         // ------------------------------------------------------------ epilogue
-        const int lg = warp & 3, uh = (warp - 4) >> 2;
-        const uint32_t lane_addr = static_cast<uint32_t>(32 * lg) << 16;
+        const int uh = (warp - 4) >> 2;
+        const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const bool hi = DUAL && lane >= 16;
+        const bool odd = lane & 1;
         const bool pair_out = a.out_type != LIN_F32 && ((a.C | a.ldo | a.o_gstride) & 1) == 0 &&
                               (reinterpret_cast<uintptr_t>(a.out[0]) & 3) == 0 &&
                               (reinterpret_cast<uintptr_t>(a.out[1]) & 3) == 0;
         const bool pair_z = ((a.C | a.ldz) & 1) == 0 && (reinterpret_cast<uintptr_t>(a.z[0]) & 3) == 0 &&
                             (reinterpret_cast<uintptr_t>(a.z[1]) & 3) == 0;
-        // 16 rows of this lane's c.  16-bit values of two rows are exchanged between neighbouring lanes so that a
-        // store carries two values: 64 bytes of each of two rows per instruction.
-        auto store16 = [&](void* ptr, long long ld, int type, bool pair, int row, int c, const float (&v)[16]) {
+        // Lane that knows the output row of this lane's value i.
+        auto row_lane = [&](int i) { return DUAL ? 2 * i + (hi ? 1 : 0) : i; };
+        // N values of this lane's c.  16-bit values of two rows are exchanged between neighbouring lanes so that a
+        // store carries two of them.
+        auto store = [&](void* ptr, long long ld, int type, bool pair, int row, int c, const auto& v) {
+            constexpr int N = sizeof(v) / sizeof(float);
             const bool on = c < a.C;
             if (type == LIN_F32) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int o = __shfl_sync(0xFFFFFFFFu, row, j);
-                    if (o >= 0 && on) static_cast<float*>(ptr)[static_cast<size_t>(o) * ld + c] = v[j];
+                for (int i = 0; i < N; ++i) {
+                    const int o = __shfl_sync(0xFFFFFFFFu, row, row_lane(i));
+                    if (o >= 0 && on) static_cast<float*>(ptr)[static_cast<size_t>(o) * ld + c] = v[i];
                 }
             } else if (pair) {
-                const bool odd = lane & 1;
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
-                    const float lo = odd ? got : v[j], hi = odd ? v[j + 1] : got;
-                    const int o = __shfl_sync(0xFFFFFFFFu, row, j + (odd ? 1 : 0));
+                for (int i = 0; i < N; i += 2) {
+                    const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 1);
+                    const float lo = odd ? got : v[i], up = odd ? v[i + 1] : got;
+                    const int o = __shfl_sync(0xFFFFFFFFu, row, row_lane(i + (odd ? 1 : 0)));
                     const uint32_t u = static_cast<uint32_t>(lin_cvt16(lo, type)) |
-                                       (static_cast<uint32_t>(lin_cvt16(hi, type)) << 16);
+                                       (static_cast<uint32_t>(lin_cvt16(up, type)) << 16);
                     if (o >= 0 && on)
                         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(ptr) + static_cast<size_t>(o) * ld +
                                                      (c & ~1)) = u;
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int o = __shfl_sync(0xFFFFFFFFu, row, j);
+                for (int i = 0; i < N; ++i) {
+                    const int o = __shfl_sync(0xFFFFFFFFu, row, row_lane(i));
                     if (o >= 0 && on)
-                        static_cast<uint16_t*>(ptr)[static_cast<size_t>(o) * ld + c] = lin_cvt16(v[j], type);
+                        static_cast<uint16_t*>(ptr)[static_cast<size_t>(o) * ld + c] = lin_cvt16(v[i], type);
                 }
             }
         };
-        // Finish 16 rows (unit `un` of the tile).
-        auto finish = [&](const LtTile& t, int un, float (&v)[16], float (&u)[16]) {
-            const int c = t.c0 + 32 * lg + lane;
+        // Finish NR rows from row `first` of the tile, lane group lg of its c.
+        auto finish = [&](const LtTile& t, int lg, int first, const auto& acc) {
+            constexpr int NR = sizeof(acc) / sizeof(float), N = DUAL ? NR / 2 : NR;
+            const int c = t.c0 + (DUAL ? 16 * lg + (lane & 15) : 32 * lg + lane);
             const bool on = c < a.C;
-            const int rr = un * 16 + (lane & 15);
-            const bool have = rr < t.nrows;
-            int grow = have ? t.r0 + rr : -1, orow = grow;
-            if (!WG && have) orow = lin_index(a.scatter, a.scatter_total, grow, a.err);
-            if (KIND == LIN_FWD) {
-                const bool bad = a.gather && have && lin_index(a.gather, a.gather_total, grow, a.err) < 0;
-                const uint32_t z = __ballot_sync(0xFFFFFFFFu, bad);
-                if (z) {   // rows that an index outside x stands for count as zero
+            const int rr = first + (lane & (NR - 1));
+            const int grow = rr < t.nrows ? t.r0 + rr : -1;
+            const int orow = !WG && grow >= 0 ? lin_index(a.scatter, a.scatter_total, grow, a.err) : grow;
+            float v[N], u[N];
+            if constexpr (DUAL) {   // gate and up of one c sit 16 lanes apart: each half takes every other row
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (z >> j & 1) v[j] = u[j] = 0.0f;
+                for (int i = 0; i < N; ++i) {
+                    const float got = __shfl_xor_sync(0xFFFFFFFFu, hi ? acc[2 * i] : acc[2 * i + 1], 16);
+                    v[i] = hi ? got : acc[2 * i];
+                    u[i] = hi ? acc[2 * i + 1] : got;
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = acc[i];
+            }
+            if (KIND == LIN_FWD) {
                 const size_t bi = static_cast<size_t>(t.e) * a.C + c;
                 if (a.bias[0] && on) {
                     const float b = lin_load(a.bias[0], bi, a.bias_type);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] += b;
+                    for (int i = 0; i < N; ++i) v[i] += b;
                 }
                 if (DUAL && a.bias[1] && on) {
                     const float b = lin_load(a.bias[1], bi, a.bias_type);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) u[j] += b;
+                    for (int i = 0; i < N; ++i) u[i] += b;
                 }
-                if (a.z[0]) store16(a.z[0], a.ldz, a.type, pair_z, grow, c, v);
-                if (DUAL && a.z[1]) store16(a.z[1], a.ldz, a.type, pair_z, grow, c, u);
-                if (DUAL) lin_act16<LACT_SWIGLU>(v, u);
-                else if (a.act == LACT_RELU) lin_act16<LACT_RELU>(v, u);
-                else if (a.act == LACT_SILU) lin_act16<LACT_SILU>(v, u);
-                else if (a.act == LACT_GELU) lin_act16<LACT_GELU>(v, u);
+                if (a.z[0]) store(a.z[0], a.ldz, a.type, pair_z, grow, c, v);
+                if (DUAL && a.z[1]) store(a.z[1], a.ldz, a.type, pair_z, grow, c, u);
+                if (DUAL) lin_act_all<LACT_SWIGLU>(v, u);
+                else if (a.act == LACT_RELU) lin_act_all<LACT_RELU>(v, v);
+                else if (a.act == LACT_SILU) lin_act_all<LACT_SILU>(v, v);
+                else if (a.act == LACT_GELU) lin_act_all<LACT_GELU>(v, v);
             }
             void* out = a.out[WG ? t.which : 0];
             if (WG) {
@@ -544,17 +774,17 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             if (res) {
                 const long long ldr = WG ? a.ldo : a.ldr;
                 const int rt = WG ? a.out_type : a.res_type;
-                float r[16];
+                float r[N];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int o = __shfl_sync(0xFFFFFFFFu, orow, j);
-                    r[j] = o >= 0 && on ? lin_load(res, static_cast<size_t>(o) * ldr + c, rt) : 0.0f;
+                for (int i = 0; i < N; ++i) {
+                    const int o = __shfl_sync(0xFFFFFFFFu, orow, row_lane(i));
+                    r[i] = o >= 0 && on ? lin_load(res, static_cast<size_t>(o) * ldr + c, rt) : 0.0f;
                 }
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] += r[j];
+                for (int i = 0; i < N; ++i) v[i] += r[i];
                 __syncwarp();   // a neighbour writes this lane's value below (res may be the output)
             }
-            store16(out, a.ldo, a.out_type, pair_out, orow, c, v);
+            store(out, a.ldo, a.out_type, pair_out, orow, c, v);
         };
         auto ld16 = [&](uint32_t addr, float (&v)[16]) {
             uint32_t r[16];
@@ -562,56 +792,67 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
         };
-        int acc = 0;
-        for (int w = blockIdx.x; w < n_work; w += G) {
+        int acc = 0, parts = 0;
+        for (int w = w0; w < n_work; w += G) {
             LtTile t;
             if (!tile_of(w, t)) continue;
-            const int units = (t.nrows + 15) / 16;
+            const int units = (t.nrows + 15) / 16, nkb = t.kb1 - t.kb0;
             auto take = [&](int ab) {
-                if (!mbar_poll(&acc_full[ab], (acc >> 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
+                if (!lt_poll<32>(&acc_full[ab], (acc >> 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
                     latch_error(a.err, ERR_ETIMEOUT, acc, KID_LINEAR);
                 tc_fence_after();
             };
             auto release = [&](int ab) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[ab]);
-            };
-            if (t.nkb == 0) {   // an empty group's gradient
-                for (int un = uh; un < units; un += 2) {
-                    float v[16], u[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = u[j] = 0.0f;
-                    finish(t, un, v, u);
+                if (lane == 0) {
+                    if (cg == 2) lt_arrive_remote(lt_map(&acc_empty[ab], 0));
+                    else mbar_arrive(&acc_empty[ab]);
                 }
-            } else if (!p.promote || t.nkb <= p.promote) {
+            };
+            // A unit of 16 rows is complete: finish it, or put this CTA's part where the others read it.
+            auto done = [&](int un, const float (&v)[16]) {
+                if (split == 1) {
+                    finish(t, warp & 3, un * 16, v);
+                } else {
+                    float* d = red + un * 16 * kLtM + 32 * (warp & 3) + lane;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) d[j * kLtM] = v[j];
+                }
+            };
+            if (split > 1 && parts > 0 &&
+                !lt_poll<16>(red_empty, (parts - 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
+                latch_error(a.err, ERR_ETIMEOUT, parts, KID_LINEAR);
+            if (nkb == 0) {   // an empty group's gradient, or nothing of a short sum
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+                for (int un = uh; un < units; un += 2) done(un, v);
+            } else if (!p.promote || nkb <= p.promote) {
                 const int ab = acc & 1;
                 take(ab);
-                const uint32_t d = tmem + lane_addr + ab * (NACC * BN);
                 for (int un = uh; un < units; un += 2) {
-                    float v[16], u[16];
-                    ld16(d + un * 16, v);
-                    if (DUAL) ld16(d + BN + un * 16, u);
-                    finish(t, un, v, u);
+                    float v[16];
+                    ld16(tmem + lane_addr + ab * BN + un * 16, v);
+                    done(un, v);
                 }
                 release(ab);
                 ++acc;
-            } else {   // fp32 output: at most 128 columns (64 of each accumulator), summed over spans in registers
-                float v[4][16];
+            } else {   // spans summed in registers
+                constexpr int NU = TMA ? 8 : 4;   // units of this warp (the element loader's CTAs have BN <= 128)
+                float v[NU][16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < NU; ++i)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[i][j] = 0.0f;
-                for (int k0 = 0; k0 < t.nkb; k0 += p.promote, ++acc) {
+                for (int k0 = 0; k0 < nkb; k0 += p.promote, ++acc) {
                     const int ab = acc & 1;
                     take(ab);
-                    const uint32_t d = tmem + lane_addr + ab * (NACC * BN);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int un = DUAL ? uh + 2 * (i & 1) : uh + 2 * i;
-                        if (un < units) {
+                    for (int i = 0; i < NU; ++i) {
+                        if (uh + 2 * i < units) {
                             float x[16];
-                            ld16(d + (DUAL && i >= 2 ? BN : 0) + un * 16, x);
+                            ld16(tmem + lane_addr + ab * BN + (uh + 2 * i) * 16, x);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) v[i][j] += x[j];
                         }
@@ -619,25 +860,51 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     release(ab);
                 }
 #pragma unroll
-                for (int i = 0; i < (DUAL ? 2 : 4); ++i) {
-                    const int un = uh + 2 * i;
-                    if (un < units) finish(t, un, v[i], v[DUAL ? i + 2 : i]);
+                for (int i = 0; i < NU; ++i)
+                    if (uh + 2 * i < units) done(uh + 2 * i, v[i]);
+            }
+            if (split > 1) {
+                lt_cluster_fence();
+                __syncwarp();
+                if (lane < split) lt_arrive_remote(lt_map(red_full, static_cast<uint32_t>(lane)));
+                if (!lt_poll<16>(red_full, parts & 1, abort_flag, a.timeout_ns) && lane == 0)
+                    latch_error(a.err, ERR_ETIMEOUT, parts, KID_LINEAR);
+                // items of four rows x one lane group over all warps of the cluster
+                for (int it = rank * kLtEpiWarps + warp - 4; it < (t.nrows + 3) / 4 * 4; it += split * kLtEpiWarps) {
+                    const int lg = it & 3, first = it >> 2 << 2;
+                    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float* at = red + first * kLtM + 32 * lg + lane;
+                    for (int s = 0; s < split; ++s) {
+                        const uint32_t from = lt_map(at, static_cast<uint32_t>(s));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] += lt_ld_cluster(from + j * kLtM * 4);
+                    }
+                    finish(t, lg, first, v);
                 }
+                __syncwarp();
+                if (lane < split) lt_arrive_remote(lt_map(red_empty, static_cast<uint32_t>(lane)));
+                ++parts;
             }
         }
     }
     tc_fence_before();
     __syncthreads();
+    if (csize > 1) lt_cluster_sync();   // no CTA leaves while another may still signal it or read its parts
     tc_fence_after();
-    if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(static_cast<uint32_t>(p.tmem_cols)));
+    if (warp == 1) {
+        if constexpr (CG == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                         "r"(static_cast<uint32_t>(p.tmem_cols)));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                         "r"(static_cast<uint32_t>(p.tmem_cols)));
+    }
 }
 
 // ------------------------------------------------------------------ host side
 // 16-bit tensor map with a 128-byte swizzle: up to three dimensions, innermost contiguous.
 inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
-                      uint64_t s2, uint32_t b1, bool rank2 = false) {
+                      uint64_t s2, uint32_t b1) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     if (!encode) {
         cudaDriverEntryPointQueryResult q;
@@ -651,7 +918,7 @@ inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0,
     const cuuint64_t strides[2] = {s1 * 2, s2 * 2};
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(kLtBK), b1, 1}, es[3] = {1, 1, 1};
     return encode(map, type == LIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                  rank2 ? 2 : 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -664,33 +931,81 @@ inline bool lt_tma_ok(const LinArgs& a) {
            (!groups || a.a_gstride % 8 == 0);
 }
 
-inline LtPlan lt_plan(const LinArgs& a, int sm_count, int smem_limit) {
-    LtPlan p{};
-    const bool dual = a.kind == LIN_FWD && a.a[1];
-    const int nacc = dual ? 2 : 1;
-    const bool f32 = a.out_type == LIN_F32;
-    p.n_ct = (a.C + kLtM - 1) / kLtM;
-    p.promote = f32 ? kLtPromote : 0;
-    int most = 256 / nacc / (f32 ? 2 : 1);
-    // rows a tile should hold: those of an average group
-    const int want = a.kind == LIN_WGRAD ? a.out_n : (a.rows + a.E - 1) / a.E;
-    p.bn = a.kind == LIN_WGRAD ? 64 : 16;
-    while (p.bn < want && p.bn < most) p.bn *= 2;
-    p.bbox = p.bn < 64 ? p.bn : 64;
-    const int btile = p.bn * 128;
-    p.stage_bytes = (nacc * kLtATile + btile + 1023) / 1024 * 1024;
-    const int head = 512 + 4 * (a.E + 1);
-    p.off_ring = (head + 1023) / 1024 * 1024;
-    p.stages = (smem_limit - 1024 - p.off_ring) / p.stage_bytes;
-    if (p.stages > kLtMaxStages) p.stages = kLtMaxStages;
-    p.smem = p.off_ring + p.stages * p.stage_bytes + 1024;
-    p.tmem_cols = 32;
-    while (p.tmem_cols < 2 * nacc * p.bn) p.tmem_cols *= 2;
-    long long tiles = static_cast<long long>(p.n_ct);
-    if (a.kind == LIN_WGRAD) tiles *= static_cast<long long>((a.out_n + p.bn - 1) / p.bn) * a.E * (a.b[1] ? 2 : 1);
-    else tiles *= a.rows / p.bn + a.E;
-    p.grid = tiles < sm_count ? static_cast<int>(tiles) : sm_count;
-    return p;
+// One candidate tile shape and what it is estimated to take, in SM cycles.
+inline double lt_shape(const LinArgs& a, bool tma, int cg, int split, int bn, int sm_count, int smem_limit, LtPlan* p) {
+    const bool dual = a.kind == LIN_FWD && a.a[1], wg = a.kind == LIN_WGRAD;
+    *p = LtPlan{};
+    p->bn = bn;
+    p->cg = cg;
+    p->split = split;
+    p->ct = dual ? kLtM / 2 : kLtM;
+    p->n_ct = (a.C + p->ct * cg - 1) / (p->ct * cg);
+    p->promote = a.out_type == LIN_F32 ? kLtPromote : 0;
+    const int brows = bn / cg;
+    p->bbox = brows < 64 ? brows : 64;
+    p->stage_bytes = kLtATile + ((wg ? (brows + 63) / 64 * 64 : brows) * 128 + 1023) / 1024 * 1024;
+    p->off_ring = (kLtOffPrefix + 4 * (a.E + 1) + 1023) / 1024 * 1024;
+    const int red = split > 1 ? bn * kLtM * 4 : 0;
+    p->stages = (smem_limit - 1024 - p->off_ring - red) / p->stage_bytes;
+    if (p->stages > kLtMaxStages) p->stages = kLtMaxStages;
+    p->off_red = p->off_ring + p->stages * p->stage_bytes;
+    p->smem = p->off_red + red + 1024;
+    p->tmem_cols = 32;
+    while (p->tmem_cols < 2 * bn) p->tmem_cols *= 2;
+    // tiles: those of a group of average size, plus half a tile for the ragged end of each
+    const int cl = cg * split;
+    double tiles, nkb, fill;
+    long long most;
+    if (wg) {
+        const int outs = a.b[1] ? 2 : 1, rt = (a.out_n + bn - 1) / bn;
+        most = static_cast<long long>(p->n_ct) * rt * a.E * outs;
+        tiles = static_cast<double>(most);
+        nkb = static_cast<double>(a.rows) / a.E / kLtBK;
+        if (nkb < 1) nkb = 1;
+        fill = static_cast<double>(a.out_n) / rt / bn;
+    } else {
+        const double groups = a.rows < a.E ? a.rows : a.E, avg = a.rows / groups;
+        double rt = a.E == 1 ? (a.rows + bn - 1) / bn : groups * (avg / bn + 0.5 > 1 ? avg / bn + 0.5 : 1.0);
+        most = static_cast<long long>(p->n_ct) * (a.rows / bn + a.E);
+        tiles = rt * p->n_ct;
+        nkb = static_cast<double>((a.Q + kLtBK - 1) / kLtBK) * (a.kind == LIN_DGRAD && a.b[1] ? 2 : 1);
+        fill = a.rows / (rt * bn);
+    }
+    if (fill > 1) fill = 1;
+    if (most > (1 << 30) || p->stages < 3) return -1;
+    const int slots = sm_count / cl;                  // clusters at a time
+    p->grid = static_cast<int>(most < slots ? most : slots) * cl;
+    // a stage: the MMAs (two cycles a column) or its bytes from L2 (~42 a cycle and SM with all of them reading)
+    const double busy = tiles * cl < sm_count ? tiles * cl / sm_count : 1.0;
+    double bytes = kLtATile + brows * 128 * fill;
+    double stage = 2.0 * bn * fill > bytes / (42 / (0.3 + 0.7 * busy)) ? 2.0 * bn * fill
+                                                                        : bytes / (42 / (0.3 + 0.7 * busy));
+    if (!tma) stage = (kLtM + brows * fill) * 16;     // element by element
+    if (stage < 150) stage = 150;
+    const double rounds = a.E == 1 || wg ? static_cast<double>((static_cast<long long>(tiles) + slots - 1) / slots)
+                                         : (tiles / slots > 1 ? tiles / slots + 0.5 : 1.0);
+    const double tile = nkb / split * stage, out = 12.0 * bn * fill;   // out: the epilogue, hidden but for the last
+    return rounds * (tile > out ? tile : out) + out / (split > 1 ? 2 : 1) + (split > 1 ? 2500 + 150 * split : 0) +
+           (cg > 1 ? 500 : 0);
+}
+
+// The shape with the smallest estimate.
+inline LtPlan lt_plan(const LinArgs& a, bool tma, int sm_count, int smem_limit) {
+    LtPlan best{}, p;
+    double least = -1;
+    const int nkb = a.kind == LIN_WGRAD ? (a.rows / a.E + kLtBK - 1) / kLtBK
+                                        : (a.Q + kLtBK - 1) / kLtBK * (a.kind == LIN_DGRAD && a.b[1] ? 2 : 1);
+    const int most = tma || a.out_type != LIN_F32 ? 256 : 128;
+    for (int cg = 1; cg <= (tma ? 2 : 1); ++cg)
+        for (int bn = (a.kind == LIN_WGRAD ? 64 : 16) * cg; bn <= most; bn *= 2)
+            for (int split = 1; split <= (cg == 1 ? 8 : 1) && (split == 1 || split * 4 <= nkb); ++split) {
+                const double t = lt_shape(a, tma, cg, split, bn, sm_count, smem_limit, &p);
+                if (t >= 0 && (least < 0 || t < least)) {
+                    least = t;
+                    best = p;
+                }
+            }
+    return best;
 }
 
 inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
@@ -700,7 +1015,7 @@ inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     bool ok = true;
     if (a.kind == LIN_WGRAD) {   // A = x [rows, C], B = dz [rows, out_n]
         const uint64_t xr = g ? a.gather_total : R;
-        ok = lt_encode(&m->a0, a.type, a.a[0], C, xr, 1, lda, lda * xr, g ? 1 : 64, g) &&
+        ok = lt_encode(&m->a0, a.type, a.a[0], C, xr, 1, lda, lda * xr, 64) &&
              lt_encode(&m->b0, a.type, a.b[0], a.out_n, R, 1, ldb, ldb * R, 64);
         m->a1 = m->a0;
         m->b1 = m->b0;
@@ -710,13 +1025,61 @@ inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     const uint64_t inner = fwd ? Q : C, outer = fwd ? C : Q;
     const uint64_t gs = E > 1 ? static_cast<uint64_t>(a.a_gstride) : lda * outer;
     const uint64_t br = g && fwd ? a.gather_total : R;
-    ok = lt_encode(&m->a0, a.type, a.a[0], inner, outer, E, lda, gs, fwd ? kLtM : 64) &&
-         lt_encode(&m->b0, a.type, a.b[0], Q, br, 1, ldb, ldb * br, g && fwd ? 1 : p.bbox, g && fwd);
+    const uint32_t abox = !fwd ? 64 : a.a[1] ? 16 : kLtM;
+    ok = lt_encode(&m->a0, a.type, a.a[0], inner, outer, E, lda, gs, abox) &&
+         lt_encode(&m->b0, a.type, a.b[0], Q, br, 1, ldb, ldb * br, p.bbox);
     m->a1 = m->a0;
     m->b1 = m->b0;
-    if (a.a[1]) ok = ok && lt_encode(&m->a1, a.type, a.a[1], inner, outer, E, lda, gs, fwd ? kLtM : 64);
+    if (a.a[1]) ok = ok && lt_encode(&m->a1, a.type, a.a[1], inner, outer, E, lda, gs, abox);
     if (a.b[1]) ok = ok && lt_encode(&m->b1, a.type, a.b[1], Q, br, 1, ldb, ldb * br, p.bbox);
     return ok;
+}
+
+// Launch the kernel a plan asks for (one translation unit per direction: linear_fwd.cu, linear_dgrad.cu,
+// linear_wgrad.cu).
+cudaError_t lin_launch_fwd(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
+cudaError_t lin_launch_dgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
+cudaError_t lin_launch_wgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
+// Let the kernels of a direction use `bytes` of dynamic shared memory on the current device.
+cudaError_t lin_allow_fwd(int bytes);
+cudaError_t lin_allow_dgrad(int bytes);
+cudaError_t lin_allow_wgrad(int bytes);
+
+template <int KIND, bool DUAL, bool TMA, int CG>
+cudaError_t lt_launch_k(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(lt_threads(TMA)));
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cg * p.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cg * p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, lin_tc_kernel<KIND, DUAL, TMA, CG>, a, p, m);
+}
+
+template <int KIND, bool DUAL>
+cudaError_t lt_launch(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
+    if (!tma) return lt_launch_k<KIND, DUAL, false, 1>(a, p, m, s);
+    return p.cg == 2 ? lt_launch_k<KIND, DUAL, true, 2>(a, p, m, s) : lt_launch_k<KIND, DUAL, true, 1>(a, p, m, s);
+}
+
+template <int KIND, bool DUAL>
+cudaError_t lt_allow(int bytes) {
+    const void* k[] = {reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 1>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 2>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, false, 1>)};
+    for (const void* f : k) {
+        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace moe

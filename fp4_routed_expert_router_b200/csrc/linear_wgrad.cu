@@ -1,0 +1,12 @@
+// linear_wgrad.cu -- the tensor-core kernels of dw = dz^T x.
+#include "linear_tc.cuh"
+
+namespace moe {
+
+cudaError_t lin_launch_wgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
+    return lt_launch<LIN_WGRAD, false>(a, p, m, tma, s);
+}
+
+cudaError_t lin_allow_wgrad(int bytes) { return lt_allow<LIN_WGRAD, false>(bytes); }
+
+}  // namespace moe

@@ -258,8 +258,6 @@ cudaError_t launch_mx(const MxArgs& a, const SlotLayout& L, const MxPlan& p, int
     return cudaLaunchKernelEx(&cfg, moe_fp4_decode_mx, a, L, p);
 }
 
-cudaError_t lin_allow_smem(int bytes);
-
 cudaError_t allow_mx_smem(int bytes) {
     return cudaFuncSetAttribute(reinterpret_cast<const void*>(moe_fp4_decode_mx),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -433,7 +431,8 @@ moe_fp4_status moe_fp4_create(const moe_fp4_config* cfg, int device, void* arena
         return bail(MOE_FP4_ENOMEM);
     }
     mx_bind(&c->mx, c->d_mx, mo, mz.cnt);
-    if (allow_mx_smem(c->smem_optin) != cudaSuccess || lin_allow_smem(c->smem_optin) != cudaSuccess ||
+    if (allow_mx_smem(c->smem_optin) != cudaSuccess || lin_allow_fwd(c->smem_optin) != cudaSuccess ||
+        lin_allow_dgrad(c->smem_optin) != cudaSuccess || lin_allow_wgrad(c->smem_optin) != cudaSuccess ||
         cudaMemset(c->d_mx, 0, mo.xp) != cudaSuccess) {   // sequence, counters, flags, zero block
         cudaGetLastError();
         return bail(MOE_FP4_ECUDA);
@@ -921,40 +920,27 @@ int64_t lin_gs(int64_t gs, int64_t rows, int64_t ld, int64_t width) {
     return gs >= (rows - 1) * ld + width ? gs : -1;
 }
 
-template <int KIND, bool DUAL>
-cudaError_t lin_launch(moe_fp4_ctx* c, const char* name, const LinArgs& a, const LtPlan& p, bool tma,
-                       const LtMaps& m, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.grid)), block(static_cast<unsigned>(lt_threads(tma)));
-    return tma ? launch_k(c, name, lin_tc_kernel<KIND, DUAL, true>, grid, block, p.smem, s, a, p, m)
-               : launch_k(c, name, lin_tc_kernel<KIND, DUAL, false>, grid, block, p.smem, s, a, p, m);
-}
-
 cudaError_t lin_run(moe_fp4_ctx* c, const char* name, const LinArgs& a, cudaStream_t s) {
-    const LtPlan p = lt_plan(a, c->sm_count, c->smem_optin);
-    if (p.stages < 2 || p.grid < 1) return cudaErrorInvalidConfiguration;
-    LtMaps m{};
     const bool tma = lt_tma_ok(a);
+    const LtPlan p = lt_plan(a, tma, c->sm_count, c->smem_optin);
+    if (p.grid < 1) return cudaErrorInvalidConfiguration;
+    LtMaps m{};
     if (tma && !lt_maps(a, p, &m)) return cudaErrorInvalidValue;
-    if (a.kind == LIN_WGRAD) return lin_launch<LIN_WGRAD, false>(c, name, a, p, tma, m, s);
-    if (a.kind == LIN_DGRAD) return lin_launch<LIN_DGRAD, false>(c, name, a, p, tma, m, s);
-    return a.a[1] ? lin_launch<LIN_FWD, true>(c, name, a, p, tma, m, s)
-                  : lin_launch<LIN_FWD, false>(c, name, a, p, tma, m, s);
-}
-
-cudaError_t lin_allow_smem(int bytes) {
-    const void* k[] = {reinterpret_cast<const void*>(lin_tc_kernel<LIN_FWD, false, true>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_FWD, false, false>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_FWD, true, true>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_FWD, true, false>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_DGRAD, false, true>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_DGRAD, false, false>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_WGRAD, false, true>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<LIN_WGRAD, false, false>)};
-    for (const void* f : k) {
-        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
+    const bool prof = c->profile && c->prof.size() < 65536;
+    cudaEvent_t ea = nullptr, eb = nullptr;
+    if (prof) {
+        ea = take_event(c);
+        eb = take_event(c);
+        cudaEventRecord(ea, s);
     }
-    return cudaSuccess;
+    const cudaError_t e = a.kind == LIN_FWD     ? lin_launch_fwd(a, p, m, tma, s)
+                          : a.kind == LIN_DGRAD ? lin_launch_dgrad(a, p, m, tma, s)
+                                                : lin_launch_wgrad(a, p, m, tma, s);
+    if (prof) {
+        cudaEventRecord(eb, s);
+        c->prof.push_back({name, ea, eb});
+    }
+    return e;
 }
 
 cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {

@@ -64,6 +64,7 @@
 #include "fp4_cvt.cuh"
 #include "slot_layout.cuh"
 #include "tma.cuh"
+#include "umma.cuh"
 
 namespace moe {
 
@@ -107,14 +108,6 @@ struct TcArgs {
 };
 
 // ------------------------------------------------------------------ PTX helpers
-__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t smem_addr) {
-    // K-major, 128-byte swizzle: start >> 4, LBO (unused) 1, SBO 1024 >> 4,
-    // descriptor version 1 (bits 46-47), layout SWIZZLE_128B = 2 (bits 61-63).
-    return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(1) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
-}
-
 __device__ __forceinline__ uint32_t umma_idesc_f16(int m, int n) {
     // D fp32 (bits 4-5 = 1), A f16 (7-9 = 0), B f16 (10-12 = 0), both
     // K-major, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
@@ -130,23 +123,6 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t r[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // 16 consecutive 32-bit columns of this thread's TMEM lane, then wait for the stores.
