@@ -24,7 +24,7 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 
 TARGETS = {
-    "libmoe_fp4.so": ["moe_fp4_api.cu", "linear_fwd.cu", "linear_dgrad.cu", "linear_wgrad.cu"],
+    "libmoe_fp4.so": ["moe_fp4_api.cu", "linear_fwd.cu", "linear_swiglu.cu", "linear_dgrad.cu", "linear_wgrad.cu"],
     "libmoe_synth.so": ["synth_fill.cu"],
 }
 

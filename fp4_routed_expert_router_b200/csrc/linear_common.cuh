@@ -66,6 +66,15 @@ __device__ __forceinline__ uint16_t lin_cvt16(float v, int type) {
     return type == LIN_BF16 ? f32_to_bf16_rne(v) : __half_as_ushort(__float2half_rn(v));
 }
 
+__device__ __forceinline__ uint32_t lin_pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t lin_pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 __device__ __forceinline__ void lin_store(void* p, size_t i, float v, int type) {
     if (type == LIN_F32) static_cast<float*>(p)[i] = v;
     else static_cast<uint16_t*>(p)[i] = lin_cvt16(v, type);

@@ -1,0 +1,12 @@
+// linear_swiglu.cu -- the tensor-core kernels of y = silu(x w^T + b) * (x w_up^T + b_up) + residual.
+#include "linear_tc.cuh"
+
+namespace moe {
+
+cudaError_t lin_launch_swiglu(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
+    return lt_launch<LIN_FWD, true>(a, p, m, tma, s);
+}
+
+cudaError_t lin_allow_swiglu(int bytes) { return lt_allow<LIN_FWD, true>(bytes); }
+
+}  // namespace moe

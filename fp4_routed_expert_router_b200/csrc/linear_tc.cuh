@@ -25,9 +25,9 @@
 //          which is what bounds a single CTA's tile here (~11 TB/s measured).
 //   single one CTA, 128 c x BN rows.
 //   split  a cluster of S CTAs shares one tile's sum when there are fewer tiles
-//          than SMs: each sums its part of q, the fp32 parts meet in shared
-//          memory (DSMEM reads in rank order, so the result does not depend on
-//          timing) and each CTA finishes its share of the rows.
+//          than SMs: each sums its part of q and pushes the fp32 values into the
+//          shared memory of the CTA that finishes their rows (DSMEM), which adds
+//          them in rank order, so the result does not depend on timing.
 //
 // Groups: rows of a tile belong to one group; a tile that ends inside a group's
 // last rows reads what lies behind them into columns that are not stored.  In
@@ -36,8 +36,7 @@
 // last row in both operands (a foreign row times zero could still be NaN).
 //
 // Persistent CTAs, one per SM.  Warps: 0 TMA loads, 1 issues the MMAs, 2-3 copy
-// gathered rows (x_rows) and ragged ends with 16-byte cp.async -- one tile::gather4 per four rows
-// and 64 values ran at 6 bytes a cycle, a quarter of the speed needed -- 4-11
+// gathered rows (x_rows, by tile::gather4) and ragged ends, 4-11
 // epilogue (TMEM lane group warp % 4, 16-column units shared by two warps), 12-15
 // (only for operands TMA cannot take: a base that is not 16-byte aligned or
 // rows that are not multiples of 8 values) load element by element.  Two
@@ -75,7 +74,6 @@ struct LtPlan {
     int bbox;       // rows of one K-major B box
     int stages, stage_bytes, off_ring, off_red, smem;
     int n_ct;       // tiles along c
-    int promote;    // stages per accumulation span (0: the whole sum)
     int tmem_cols;
     int grid;       // CTAs
 };
@@ -141,8 +139,10 @@ __device__ __forceinline__ uint32_t lt_map(const void* p, uint32_t rank) {
     return r;
 }
 
+// Arrive at a barrier anywhere in the cluster.  (Without .release.cluster, which waits for every earlier store of the
+// thread to be visible there; what has to be is ordered by lt_cluster_fence, once per tile.)
 __device__ __forceinline__ void lt_arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void lt_cluster_sync() {
@@ -150,8 +150,7 @@ __device__ __forceinline__ void lt_cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Bounded wait for phase `parity` of `bar` that also orders what other CTAs of the cluster wrote before they
-// arrived.  The probes come without a pause (SLEEP = 0, the two warps whose pace sets the kernel's) or SLEEP ns apart;
+// Bounded wait for phase `parity` of `bar`.  The probes come without a pause (SLEEP = 0, the two warps whose pace sets the kernel's) or SLEEP ns apart;
 // the timer, whose reading costs about as much as a stage, is looked at every 256 probes only.
 template <int SLEEP>
 __device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
@@ -161,7 +160,7 @@ __device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
             : "r"(at), "r"(parity)
@@ -180,10 +179,8 @@ __device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile
     }
 }
 
-__device__ __forceinline__ float lt_ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void lt_st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ void lt_cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
@@ -206,8 +203,30 @@ __device__ __forceinline__ void lt_tma3(uint32_t dst, const CUtensorMap* map, in
 }
 
 // 16 bytes, of which the last 16 - n are zeros.
-__device__ __forceinline__ void lt_cp16(uint8_t* dst, const void* src, int n) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+__device__ __forceinline__ void lt_cp16(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// Four rows (any rows) x 64 values; the map's box is one row high.
+template <int CG>
+__device__ __forceinline__ void lt_gather4(uint32_t dst, const CUtensorMap* map, int c0, int4 r, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 "
+            "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+            : "memory");
+}
+
+// Arrive at a barrier anywhere in the cluster and announce `bytes` of copies that complete on it.
+__device__ __forceinline__ void lt_arrive_expect_remote(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // One lane of a converged warp.  The compiler then knows that a single thread issues TMA and MMA instructions; behind
@@ -230,6 +249,31 @@ struct LtRing {
     }
 };
 
+// Eight 16-bit values from any 2-byte aligned address, zeros from value n on: the widest loads that stay inside them.
+__device__ __forceinline__ uint4 lt_chunk(const uint16_t* s, int n) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (n >= 8) {
+        const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s));
+        if ((at & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(s));
+        if ((at & 3) == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
+        } else {
+            const uint32_t* m = reinterpret_cast<const uint32_t*>(s + 1);
+            const uint32_t a = __ldg(s), b = __ldg(m), c = __ldg(m + 1), d = __ldg(m + 2), e = __ldg(s + 7);
+            w[0] = a | b << 16;
+            w[1] = __funnelshift_l(b, c, 16);
+            w[2] = __funnelshift_l(c, d, 16);
+            w[3] = d >> 16 | e << 16;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < n) w[i >> 1] |= static_cast<uint32_t>(__ldg(s + i)) << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 struct LtTile {
     int e, which;   // group, output (wgrad: dw or dw_up)
     int c0;         // first c of this CTA
@@ -241,7 +285,7 @@ struct LtTile {
     int nb;         // B rows of this CTA's stage
 };
 
-template <int KIND, bool DUAL, bool TMA, int CG>
+template <int KIND, bool DUAL, bool TMA, int CG, bool SPANS>
 __global__ void __launch_bounds__(lt_threads(TMA), 1)
 lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps maps) {
     constexpr bool WG = KIND == LIN_WGRAD;
@@ -264,7 +308,8 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     uint64_t* red_empty = red_full + 1;                    // and has been read
     int* src_row = reinterpret_cast<int*>(smem + kLtOffIdx);
     int* tprefix = reinterpret_cast<int*>(smem + kLtOffPrefix);   // [E+1] tiles before group e (forward, dgrad)
-    float* red = reinterpret_cast<float*>(smem + p.off_red);      // [BN][128] this CTA's part (split)
+    // split: the parts of this CTA's items (four rows x 32 lanes), [round * warps + warp][rank][4][32]
+    float* red = reinterpret_cast<float*>(smem + p.off_red);
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     volatile int* abort_flag = &abort_s;
@@ -387,6 +432,11 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     auto stage_b = [&](int st) { return stage_a(st) + kLtATile; };
     const int half_kb = (a.Q + kLtBK - 1) / kLtBK;   // dgrad: stages of the first pair
     const uint32_t ring0 = smem_u32(smem + p.off_ring);
+    const bool epilogue = warp >= 4 && warp < 4 + kLtEpiWarps;
+    // The epilogue of the span kernels holds a tile's sums in registers: 128 a thread on top of its work.  384 threads
+    // start with 168 each; 128 x 56 + 256 x 224 is the same number.
+    if (!epilogue) {
+    if constexpr (SPANS && TMA) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (TMA && warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lt_elect()) {
@@ -458,15 +508,18 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
         }
     } else if (copies && (warp == 2 || warp == 3)) {
         // ------------------------------------------------------------ gathered rows and ragged ends (64 threads)
-        // forward: the tile's B rows, 8 chunks of 16 bytes each; wgrad: the stage's 64 A rows (2 x 8 chunks) and, in a
-        // group's last stage, its B rows too.  A stage is handed over once its copies have landed, `lag` stages later.
-        const int lt = tid - 64;
+        // Gathered rows (forward: the tile's B rows; wgrad: the stage's 64 A rows) come by tile::gather4, four rows x 64
+        // values each, half of them issued by each warp.  Stages that need zeros -- an index that is no row of x, a
+        // group's last stage in wgrad (there both operands) -- are copied in 16-byte pieces and handed over one stage
+        // later, when they have landed.
+        const int lt = tid - 64, wi = warp - 2;
         const uint16_t* xb = static_cast<const uint16_t*>(WG ? a.a[0] : a.b[0]);
         const long long ldx = WG ? a.lda : a.ldb;
-        const uint32_t bar0 = cg == 2 ? lt_map(full, 0) : lt_map(full, static_cast<uint32_t>(rank));
-        const int lag = S >= 6 ? 3 : 1;
-        LtRing ring, out;
-        int g = 0, given = 0;
+        const CUtensorMap* xmap = WG ? &maps.a0 : &maps.b0;
+        const uint32_t bar0 = cg == 2 ? lt_map(full, 0) : smem_u32(full);
+        LtRing ring;
+        int turn = 0;
+        int pending = -1;            // slot of a copied stage that has not been handed over
         bool stop = false;
         auto source = [&](int r) {   // row of x behind grouped row r, -1: counts as zero
             if (!a.gather) return r;
@@ -475,16 +528,9 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             latch_error(a.err, ERR_EINVAL, r, KID_LINEAR);
             return -1;
         };
-        auto slot_free = [&](const LtRing& at) {   // (warp-uniform)
-            int ok = 1;
-            if (lane == 0) {
-                ok = lt_poll<0>(&empty[at.st], at.ph ^ 1, abort_flag, a.timeout_ns);
-                if (!ok) latch_error(a.err, ERR_ETIMEOUT, g, KID_LINEAR);
-            }
-            return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
-        };
-        auto both = [&](bool ok) {   // meet the other warp; whether both are fine
+        auto both = [&](bool ok) {   // meet the other warp; whether all threads of both are fine
             uint32_t r;
+            __syncwarp();
             asm volatile(
                 "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
                 "barrier.cta.red.and.aligned.pred q, 1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
@@ -493,14 +539,14 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 : "memory");
             return r != 0;
         };
-        auto give = [&]() {          // the oldest stage not yet handed over has landed
+        auto hand_over = [&]() {
+            if (pending < 0) return;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) lt_arrive_remote(bar0 + out.st * 8);
-            out.next(S);
-            ++given;
+            if (lane == 0) lt_arrive_remote(bar0 + pending * 8);
+            pending = -1;
         };
-        auto copy = [&](uint8_t* tile, int row, int ch, const uint16_t* base, long long ld, int r, int col, int width) {
+        auto copy = [&](uint32_t tile, int row, int ch, const uint16_t* base, long long ld, int r, int col, int width) {
             const int n = r < 0 ? 0 : max(0, min(16, (width - col) * 2));
             lt_cp16(tile + row * 128 + ((ch ^ (row & 7)) << 4),
                     n == 0 ? base : base + static_cast<size_t>(r) * ld + col, n);
@@ -508,57 +554,106 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
         for (int w = w0; w < n_work && !stop; w += G) {
             LtTile t;
             if (!tile_of(w, t)) continue;
+            bool sound = true;                   // every index is a row of x
+            const int need = max(0, min(t.nb, t.nrows - t.b0));   // forward: rows of this CTA that count
             if (!WG) {
-                asm volatile("bar.sync 1, 64;" ::: "memory");
+                both(true);                      // the other warp is done with the last tile's table
                 for (int i = lt; i < t.nb; i += 64) {
-                    const int r = t.b0 + i;
-                    src_row[i] = r < t.nrows ? source(t.r0 + r) : -1;
+                    const int v = i < need ? source(t.r0 + t.b0 + i) : -1;
+                    sound &= v >= 0 || i >= need;
+                    src_row[i] = v;
                 }
-                asm volatile("bar.sync 1, 64;" ::: "memory");
+                sound = both(sound);
             }
-            for (int kb = t.kb0; kb < t.kb1; ++kb, ++g, ring.next(S)) {
-                const int st = ring.st;
+            int ahead = WG && gathers && lt < t.nq - t.kb0 * kLtBK && t.kb0 < t.kb1
+                            ? source(t.p0 + t.kb0 * kLtBK + lt) : WG && !gathers ? t.p0 + t.kb0 * kLtBK + lt : -1;
+            for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next(S)) {
                 const int valid = t.nq - kb * kLtBK;
                 const bool ragged = WG && valid < kLtBK;
-                const bool mine = gathers || ragged;
-                // two tables in turn: the other one may still be read
-                if (WG && mine) src_row[(g & 1) * 64 + lt] = lt < valid ? source(t.p0 + kb * kLtBK + lt) : -1;
-                if (!both(slot_free(ring))) {
+                int* table = src_row;
+                if (WG) {
+                    table += turn * 64;
+                    turn ^= 1;
+                }
+                if (WG) {   // two tables in turn: the other one may still be read
+                    sound = ahead >= 0;
+                    table[lt] = lt < valid ? ahead : -1;
+                    const int q = (kb + 1) * kLtBK + lt;
+                    if (gathers) ahead = kb + 1 < t.kb1 && q < t.nq ? source(t.p0 + q) : -1;
+                    else ahead = t.p0 + q;
+                }
+                bool ok = true;
+                if (lane == 0) {
+                    ok = lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, a.timeout_ns);
+                    if (!ok) latch_error(a.err, ERR_ETIMEOUT, kb, KID_LINEAR);
+                }
+                if (!both(ok)) {
                     stop = true;
                     break;
                 }
-                if (mine && !WG) {
+                if (WG) sound = both(sound || ragged);
+                const uint32_t sa = ring0 + ring.st * p.stage_bytes, sb = sa + kLtATile, bar = bar0 + ring.st * 8;
+                if (!ragged && (!gathers || sound)) {
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    hand_over();
+                    if (lt_elect()) {
+                        if (!gathers) {
+                            lt_arrive_remote(bar);
+                        } else if (!WG) {
+                            const int quads = (need + 3) / 4, mine = (quads + 1 - wi) / 2;
+                            lt_arrive_expect_remote(bar, static_cast<uint32_t>(mine * 512));
+                            for (int q = wi; q < quads; q += 2) {
+                                int4 r = *reinterpret_cast<const int4*>(table + 4 * q);   // behind the last: row 0
+                                r.y = max(r.y, 0);
+                                r.z = max(r.z, 0);
+                                r.w = max(r.w, 0);
+                                lt_gather4<CG>(sb + q * 512, xmap, kb * kLtBK, r, bar);
+                            }
+                        } else {
+                            const int c = t.c0 + 64 * wi;
+                            lt_arrive_expect_remote(bar, c < a.C ? 8192u : 0u);
+                            if (c < a.C) {
+#pragma unroll 4
+                                for (int q = 0; q < 16; ++q)
+                                    lt_gather4<CG>(sa + wi * 8192 + q * 512, xmap, c,
+                                                   *reinterpret_cast<const int4*>(table + 4 * q), bar);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    continue;
+                }
+                if (!WG) {
+#pragma unroll 4
                     for (int i = lt >> 3; i < t.nb; i += 8)
-                        copy(stage_b(st), i, lt & 7, xb, ldx, src_row[i], kb * kLtBK + (lt & 7) * 8, a.Q);
-                } else if (mine) {
+                        copy(sb, i, lt & 7, xb, ldx, table[i], kb * kLtBK + (lt & 7) * 8, a.Q);
+                } else {
                     const int rows = ragged ? (valid + 15) / 16 * 16 : kLtBK;
                     const int ch = lt & 15;
 #pragma unroll 4
                     for (int i = lt >> 4; i < rows; i += 4)
-                        copy(stage_a(st) + (ch >> 3) * 8192, i, ch & 7, xb, ldx, src_row[(g & 1) * 64 + i],
-                             t.c0 + ch * 8, a.C);
+                        copy(sa + (ch >> 3) * 8192, i, ch & 7, xb, ldx, table[i], t.c0 + ch * 8, a.C);
                     if (ragged) {
                         const uint16_t* bb = static_cast<const uint16_t*>(a.b[t.which]);
-                        const int nch = (t.nb + 63) / 64 * 8;
-                        for (int i = lt; i < rows * nch; i += 64) {
-                            const int row = i / nch, c = i - row * nch;
-                            copy(stage_b(st) + (c >> 3) * 8192, row, c & 7, bb, a.ldb,
-                                 row < valid ? t.p0 + kb * kLtBK + row : -1, t.r0 + t.b0 + c * 8, a.out_n);
+                        const int per = (t.nb + 63) / 64 * 8;   // chunks of a row: 8, 16 or 32 (24: taken as 32)
+                        const int shift = per <= 8 ? 3 : per <= 16 ? 4 : 5;
+#pragma unroll 4
+                        for (int i = lt; i < rows << shift; i += 64) {
+                            const int row = i >> shift, c = i & ((1 << shift) - 1);
+                            if (c < per)
+                                copy(sb + (c >> 3) * 8192, row, c & 7, bb, a.ldb,
+                                     row < valid ? t.p0 + kb * kLtBK + row : -1, t.r0 + t.b0 + c * 8, a.out_n);
                         }
                     }
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                if (!gathers && !ragged) {
-                    while (given <= g) give();   // nothing of this stage is in flight here
-                } else if (g - given >= lag) {
-                    if (lag == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-                    else asm volatile("cp.async.wait_group 1;" ::: "memory");
-                    give();
-                }
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                hand_over();
+                pending = ring.st;
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        while (given < g) give();
+        hand_over();
     } else if (!TMA && warp >= 4 + kLtEpiWarps) {
         // ------------------------------------------------------------ element loader (128 threads)
         const int lt = tid - (4 + kLtEpiWarps) * 32;
@@ -579,16 +674,14 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 const bool second = KIND == LIN_DGRAD && kb >= half_kb;
                 const int q0 = (second ? kb - half_kb : kb) * kLtBK;
                 const int nq = min(kLtBK, t.nq - q0);
-                // a row of 64 contiguous values (zeros from n on; n <= 0 or no row: all zeros) into swizzled row `sr`
-                // of a tile: half a warp per row, two rows a step
-                auto put = [&](uint8_t* tile, int sr, int col, uint16_t v) {
-                    *reinterpret_cast<uint16_t*>(tile + sr * 128 + (((col >> 3) ^ (sr & 7)) << 4) + (col & 7) * 2) = v;
-                };
+                // rows of 64 contiguous values (zeros from n on, or where there is no row), a chunk of eight a thread
                 auto fill = [&](uint8_t* tile, int rows, auto src_of, int n) {
-                    for (int i = lt; i < rows * 64; i += 128) {
-                        const int sr = i >> 6, col = i & 63;
+#pragma unroll 4
+                    for (int i = lt; i < rows * 8; i += 128) {
+                        const int sr = i >> 3, ch = i & 7;
                         const uint16_t* s = src_of(sr);
-                        put(tile, sr, col, s && col < n ? __ldg(s + col) : static_cast<uint16_t>(0));
+                        *reinterpret_cast<uint4*>(tile + sr * 128 + ((ch ^ (sr & 7)) << 4)) =
+                            lt_chunk(s ? s + ch * 8 : nullptr, s ? n - ch * 8 : 0);
                     }
                 };
                 uint8_t* sa = stage_a(st);
@@ -649,7 +742,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 LtTile t;
                 if (!tile_of(w, t)) continue;
                 const uint32_t idesc = lt_idesc(a.type, A_MN, WG, kLtM * cg, t.n);
-                const int span = p.promote ? p.promote : t.kb1 - t.kb0;
+                const int span = SPANS ? kLtPromote : t.kb1 - t.kb0;
                 for (int k0 = t.kb0; k0 < t.kb1; k0 += span, ++acc) {
                     const int ab = acc & 1;
                     if (!lt_poll<0>(&acc_empty[ab], ((acc >> 1) & 1) ^ 1, abort_flag, a.timeout_ns))
@@ -680,117 +773,181 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     mbar_wait(&acc_full[(acc - k) & 1], ((acc - k) >> 1) & 1, &fresh);
                 }
         }
-    } else if (warp >= 4 && warp < 4 + kLtEpiWarps) {
+    }
+    } else {
         // ------------------------------------------------------------ epilogue
+        if constexpr (SPANS && TMA) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        // A block of NR rows: this lane has NR values of one c; for SwiGLU gate and up of every other row of one c.
         const int uh = (warp - 4) >> 2;
         const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const bool hi = DUAL && lane >= 16;
-        const bool odd = lane & 1;
+        constexpr int RS = DUAL ? 2 : 1;                    // rows between a lane's neighbouring values
+        const int h = DUAL && lane >= 16 ? 1 : 0;           // its first row
+        const int odd = lane & 1;
+        const uint32_t pick = odd ? 0x3276u : 0x5410u;      // even lanes keep a pair's first row, odd ones its second
         const bool pair_out = a.out_type != LIN_F32 && ((a.C | a.ldo | a.o_gstride) & 1) == 0 &&
                               (reinterpret_cast<uintptr_t>(a.out[0]) & 3) == 0 &&
                               (reinterpret_cast<uintptr_t>(a.out[1]) & 3) == 0;
         const bool pair_z = ((a.C | a.ldz) & 1) == 0 && (reinterpret_cast<uintptr_t>(a.z[0]) & 3) == 0 &&
                             (reinterpret_cast<uintptr_t>(a.z[1]) & 3) == 0;
-        // Lane that knows the output row of this lane's value i.
-        auto row_lane = [&](int i) { return DUAL ? 2 * i + (hi ? 1 : 0) : i; };
-        // N values of this lane's c.  16-bit values of two rows are exchanged between neighbouring lanes so that a
-        // store carries two of them.
-        auto store = [&](void* ptr, long long ld, int type, bool pair, int row, int c, const auto& v) {
+        const void* res_all = WG ? (a.accumulate ? a.out[0] : nullptr) : a.res;
+        const long long ldr = WG ? a.ldo : a.ldr;
+        const int res_type = WG ? a.out_type : a.res_type;
+        const bool pair_res = res_type != LIN_F32 && ((a.C | ldr) & 1) == 0 &&
+                              (WG ? pair_out : (reinterpret_cast<uintptr_t>(a.res) & 3) == 0);
+        // N values into rows row0 + h + RS i (or, indexed, the rows that lane h + RS i holds in orow); rows from `valid`
+        // on are left.  16-bit values are packed by row pairs and exchanged with the neighbouring lane, so that a store
+        // carries two c of one row.
+        auto store = [&](void* ptr, long long ld, int type, bool pair, bool indexed, int orow, int row0, int valid, int c,
+                         const auto& v) {
             constexpr int N = sizeof(v) / sizeof(float);
             const bool on = c < a.C;
             if (type == LIN_F32) {
+                float* d = static_cast<float*>(ptr) + c;
+                if (!indexed) {
+                    d += static_cast<long long>(row0 + h) * ld;
+                    const int left = on ? valid - h : 0;
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int o = __shfl_sync(0xFFFFFFFFu, row, row_lane(i));
-                    if (o >= 0 && on) static_cast<float*>(ptr)[static_cast<size_t>(o) * ld + c] = v[i];
+                    for (int i = 0; i < N; ++i, d += RS * ld)
+                        if (RS * i < left) *d = v[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int o = __shfl_sync(0xFFFFFFFFu, orow, RS * i + h);
+                        if (o >= 0 && on) d[static_cast<long long>(o) * ld] = v[i];
+                    }
                 }
             } else if (pair) {
+                uint32_t w[N / 2];
+                if (type == LIN_BF16) {
 #pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 1);
-                    const float lo = odd ? got : v[i], up = odd ? v[i + 1] : got;
-                    const int o = __shfl_sync(0xFFFFFFFFu, row, row_lane(i + (odd ? 1 : 0)));
-                    const uint32_t u = static_cast<uint32_t>(lin_cvt16(lo, type)) |
-                                       (static_cast<uint32_t>(lin_cvt16(up, type)) << 16);
-                    if (o >= 0 && on)
-                        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(ptr) + static_cast<size_t>(o) * ld +
-                                                     (c & ~1)) = u;
+                    for (int i = 0; i < N / 2; ++i) w[i] = lin_pack_bf16(v[2 * i], v[2 * i + 1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) w[i] = lin_pack_f16(v[2 * i], v[2 * i + 1]);
+                }
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i)
+                    w[i] = __byte_perm(w[i], __shfl_xor_sync(0xFFFFFFFFu, w[i], 1), pick);
+                uint16_t* d = static_cast<uint16_t*>(ptr) + (c & ~1);
+                if (!indexed) {
+                    d += static_cast<long long>(row0 + h + RS * odd) * ld;
+                    const int left = on ? valid - h - RS * odd : 0;
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i, d += 2 * RS * ld)
+                        if (2 * RS * i < left) *reinterpret_cast<uint32_t*>(d) = w[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) {
+                        const int o = __shfl_sync(0xFFFFFFFFu, orow, RS * (2 * i + odd) + h);
+                        if (o >= 0 && on) *reinterpret_cast<uint32_t*>(d + static_cast<long long>(o) * ld) = w[i];
+                    }
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int o = __shfl_sync(0xFFFFFFFFu, row, row_lane(i));
+                    const int o = indexed ? __shfl_sync(0xFFFFFFFFu, orow, RS * i + h)
+                                          : (RS * i + h < valid ? row0 + RS * i + h : -1);
                     if (o >= 0 && on)
-                        static_cast<uint16_t*>(ptr)[static_cast<size_t>(o) * ld + c] = lin_cvt16(v[i], type);
+                        static_cast<uint16_t*>(ptr)[static_cast<long long>(o) * ld + c] = lin_cvt16(v[i], type);
                 }
             }
         };
-        // Finish NR rows from row `first` of the tile, lane group lg of its c.
-        auto finish = [&](const LtTile& t, int lg, int first, const auto& acc) {
-            constexpr int NR = sizeof(acc) / sizeof(float), N = DUAL ? NR / 2 : NR;
-            const int c = t.c0 + (DUAL ? 16 * lg + (lane & 15) : 32 * lg + lane);
+        // What `store` would write over in the residual, as it lies there (fp32: one value a register, pairs: one word
+        // for two values, else one 16-bit value a register).
+        auto load_res = [&](const void* ptr, bool indexed, int orow, int row0, int valid, int c, auto& raw) {
+            constexpr int N = sizeof(raw) / sizeof(uint32_t);
             const bool on = c < a.C;
-            const int rr = first + (lane & (NR - 1));
-            const int grow = rr < t.nrows ? t.r0 + rr : -1;
-            const int orow = !WG && grow >= 0 ? lin_index(a.scatter, a.scatter_total, grow, a.err) : grow;
+            if (pair_res) {
+                const uint16_t* d = static_cast<const uint16_t*>(ptr) + (c & ~1);
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const int r = RS * (2 * i + odd) + h;
+                    const int o = indexed ? __shfl_sync(0xFFFFFFFFu, orow, r) : (r < valid ? row0 + r : -1);
+                    raw[i] = o >= 0 && on ? *reinterpret_cast<const uint32_t*>(d + static_cast<long long>(o) * ldr) : 0u;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int r = RS * i + h;
+                    const int o = indexed ? __shfl_sync(0xFFFFFFFFu, orow, r) : (r < valid ? row0 + r : -1);
+                    const long long at = static_cast<long long>(o) * ldr + c;
+                    raw[i] = 0u;
+                    if (o >= 0 && on)
+                        raw[i] = res_type == LIN_F32 ? static_cast<const uint32_t*>(ptr)[at]
+                                                     : static_cast<const uint16_t*>(ptr)[at];
+                }
+            }
+        };
+        auto cvt_res = [&](uint32_t b) {
+            return res_type == LIN_F32    ? __uint_as_float(b)
+                   : res_type == LIN_BF16 ? bf16_to_f32(static_cast<uint16_t>(b))
+                                          : __half2float(__ushort_as_half(static_cast<uint16_t>(b)));
+        };
+        auto add_res = [&](const auto& raw, auto& v) {
+            constexpr int N = sizeof(v) / sizeof(float);
+            if (pair_res) {
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, raw[i], 1);
+                    v[2 * i] += cvt_res(odd ? got >> 16 : raw[i] & 0xFFFF);
+                    v[2 * i + 1] += cvt_res(odd ? raw[i] >> 16 : got & 0xFFFF);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += cvt_res(raw[i]);
+            }
+        };
+        // c of this lane in lane group lg, and the bias there
+        auto col = [&](const LtTile& t, int lg) { return t.c0 + (DUAL ? 16 * lg + (lane & 15) : 32 * lg + lane); };
+        auto bias_of = [&](const LtTile& t, int m, int c) {
+            return KIND == LIN_FWD && a.bias[m] && c < a.C
+                       ? lin_load(a.bias[m], static_cast<size_t>(t.e) * a.C + c, a.bias_type) : 0.0f;
+        };
+        // Output rows of NR rows from row `first` of the tile, when they are indexed: lane i has row i's.
+        auto rows_of = [&](const LtTile& t, int first, int nr) {
+            const int r = first + (lane & (nr - 1));
+            return !WG && a.scatter && r < t.nrows ? lin_index(a.scatter, a.scatter_total, t.r0 + r, a.err) : -1;
+        };
+        auto out_of = [&](const LtTile& t, void* out) -> void* {
+            if (!WG) return out;
+            const size_t skip = static_cast<size_t>(t.e) * a.o_gstride;
+            return a.out_type == LIN_F32 ? static_cast<void*>(static_cast<float*>(out) + skip)
+                                         : static_cast<void*>(static_cast<uint16_t*>(out) + skip);
+        };
+        // Finish NR rows from row `first` of the tile; raw: the residual (load_res), if there is one.
+        auto finish = [&](const LtTile& t, int c, int first, int orow, float b0, float b1, const auto& acc,
+                          const auto& raw) {
+            constexpr int NR = sizeof(acc) / sizeof(float), N = NR / RS;
+            const int row0 = t.r0 + first, valid = t.nrows - first;
             float v[N], u[N];
             if constexpr (DUAL) {   // gate and up of one c sit 16 lanes apart: each half takes every other row
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const float got = __shfl_xor_sync(0xFFFFFFFFu, hi ? acc[2 * i] : acc[2 * i + 1], 16);
-                    v[i] = hi ? got : acc[2 * i];
-                    u[i] = hi ? acc[2 * i + 1] : got;
+                    const float got = __shfl_xor_sync(0xFFFFFFFFu, h ? acc[2 * i] : acc[2 * i + 1], 16);
+                    v[i] = (h ? got : acc[2 * i]) + b0;
+                    u[i] = (h ? acc[2 * i + 1] : got) + b1;
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[i] = acc[i];
+                for (int i = 0; i < N; ++i) v[i] = acc[i] + b0;
             }
             if (KIND == LIN_FWD) {
-                const size_t bi = static_cast<size_t>(t.e) * a.C + c;
-                if (a.bias[0] && on) {
-                    const float b = lin_load(a.bias[0], bi, a.bias_type);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) v[i] += b;
-                }
-                if (DUAL && a.bias[1] && on) {
-                    const float b = lin_load(a.bias[1], bi, a.bias_type);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) u[i] += b;
-                }
-                if (a.z[0]) store(a.z[0], a.ldz, a.type, pair_z, grow, c, v);
-                if (DUAL && a.z[1]) store(a.z[1], a.ldz, a.type, pair_z, grow, c, u);
+                if (a.z[0]) store(a.z[0], a.ldz, a.type, pair_z, false, 0, row0, valid, c, v);
+                if (DUAL && a.z[1]) store(a.z[1], a.ldz, a.type, pair_z, false, 0, row0, valid, c, u);
                 if (DUAL) lin_act_all<LACT_SWIGLU>(v, u);
                 else if (a.act == LACT_RELU) lin_act_all<LACT_RELU>(v, v);
                 else if (a.act == LACT_SILU) lin_act_all<LACT_SILU>(v, v);
                 else if (a.act == LACT_GELU) lin_act_all<LACT_GELU>(v, v);
             }
-            void* out = a.out[WG ? t.which : 0];
-            if (WG) {
-                const size_t skip = static_cast<size_t>(t.e) * a.o_gstride;
-                out = a.out_type == LIN_F32 ? static_cast<void*>(static_cast<float*>(out) + skip)
-                                            : static_cast<void*>(static_cast<uint16_t*>(out) + skip);
-            }
-            const void* res = WG ? (a.accumulate ? out : nullptr) : a.res;
-            if (res) {
-                const long long ldr = WG ? a.ldo : a.ldr;
-                const int rt = WG ? a.out_type : a.res_type;
-                float r[N];
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int o = __shfl_sync(0xFFFFFFFFu, orow, row_lane(i));
-                    r[i] = o >= 0 && on ? lin_load(res, static_cast<size_t>(o) * ldr + c, rt) : 0.0f;
-                }
-#pragma unroll
-                for (int i = 0; i < N; ++i) v[i] += r[i];
-                __syncwarp();   // a neighbour writes this lane's value below (res may be the output)
-            }
-            store(out, a.ldo, a.out_type, pair_out, orow, c, v);
+            if (res_all) add_res(raw, v);
+            store(out_of(t, a.out[WG ? t.which : 0]), a.ldo, a.out_type, pair_out, !WG && a.scatter, orow, row0, valid,
+                  c, v);
         };
-        auto ld16 = [&](uint32_t addr, float (&v)[16]) {
-            uint32_t r[16];
-            tmem_ld16(addr, r);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+        auto residual = [&](const LtTile& t, int c, int first, int orow, auto& raw) {
+            if (!res_all) return;
+            const void* r = WG ? out_of(t, a.out[t.which]) : a.res;
+            load_res(r, !WG && a.scatter, orow, t.r0 + first, t.nrows - first, c, raw);
+            __syncwarp();   // (the residual may be the output: a neighbour writes this lane's value)
         };
         int acc = 0, parts = 0;
         for (int w = w0; w < n_work; w += G) {
@@ -810,58 +967,106 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     else mbar_arrive(&acc_empty[ab]);
                 }
             };
-            // A unit of 16 rows is complete: finish it, or put this CTA's part where the others read it.
-            auto done = [&](int un, const float (&v)[16]) {
-                if (split == 1) {
-                    finish(t, warp & 3, un * 16, v);
-                } else {
-                    float* d = red + un * 16 * kLtM + 32 * (warp & 3) + lane;
+            constexpr int NV = 16 / RS;
+            const int c = col(t, warp & 3);
+            const float b0 = bias_of(t, 0, c), b1 = DUAL ? bias_of(t, 1, c) : 0.0f;
+            // Send each item of four rows of a unit to the CTA that finishes it.
+            auto send = [&](int un, const float (&v)[16]) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) d[j * kLtM] = v[j];
+                for (int q = 0; q < 4; ++q) {
+                    const int it = (un * 4 + q) * 4 + (warp & 3), to = it / kLtEpiWarps % split;
+                    const int at = it / (kLtEpiWarps * split) * kLtEpiWarps + it % kLtEpiWarps;
+                    const uint32_t d = lt_map(red + (at * split + rank) * 128 + lane, static_cast<uint32_t>(to));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) lt_st_cluster(d + j * 128, v[4 * q + j]);
+                }
+            };
+            // The tile's units of this warp, one after the other: `get(i, un, v)` gives the sums of the i-th, un; the
+            // next unit's residual is on its way meanwhile.
+            auto units_do = [&](auto get) {
+                constexpr bool AHEAD = !SPANS;   // (the span kernels have no registers left for it)
+                uint32_t raw[NV], next[NV];
+                int orow = 0;
+                if (AHEAD) {
+                    orow = rows_of(t, uh * 16, 16);
+                    if (split == 1 && uh < units) residual(t, c, uh * 16, orow, next);
+                }
+#pragma unroll 1
+                for (int un = uh; un < units; un += 2) {
+                    float v[16];
+                    int now = orow;
+                    if constexpr (AHEAD) {
+#pragma unroll
+                        for (int k = 0; k < NV; ++k) raw[k] = next[k];
+                        if (un + 2 < units) {
+                            orow = rows_of(t, (un + 2) * 16, 16);
+                            if (split == 1) residual(t, c, (un + 2) * 16, orow, next);
+                        }
+                    } else if (split == 1) {
+                        now = rows_of(t, un * 16, 16);
+                        residual(t, c, un * 16, now, raw);
+                    }
+                    get(un, v);
+                    if (split == 1) finish(t, c, un * 16, now, b0, b1, v, raw);
+                    else send(un, v);
                 }
             };
             if (split > 1 && parts > 0 &&
                 !lt_poll<16>(red_empty, (parts - 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
                 latch_error(a.err, ERR_ETIMEOUT, parts, KID_LINEAR);
             if (nkb == 0) {   // an empty group's gradient, or nothing of a short sum
-                float v[16];
+                units_do([&](int, float (&v)[16]) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = 0.0f;
-                for (int un = uh; un < units; un += 2) done(un, v);
-            } else if (!p.promote || nkb <= p.promote) {
+                    for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+                });
+            } else if (!SPANS || nkb <= kLtPromote) {
                 const int ab = acc & 1;
-                take(ab);
-                for (int un = uh; un < units; un += 2) {
-                    float v[16];
-                    ld16(tmem + lane_addr + ab * BN + un * 16, v);
-                    done(un, v);
-                }
+                bool ready = false;
+                uint32_t r[16];
+                units_do([&](int un, float (&v)[16]) {
+                    const uint32_t at = tmem + lane_addr + ab * BN + un * 16;
+                    if (!ready) {
+                        take(ab);
+                        ready = true;
+                        tmem_ld16_start(at, r);
+                    }
+                    tmem_ld16_wait(r);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+                    if (un + 2 < units) tmem_ld16_start(at + 32, r);   // lands while this unit is finished
+                });
+                if (!ready) take(ab);
                 release(ab);
                 ++acc;
-            } else {   // spans summed in registers
-                constexpr int NU = TMA ? 8 : 4;   // units of this warp (the element loader's CTAs have BN <= 128)
+            } else if constexpr (SPANS) {   // spans summed in registers
+                constexpr int NU = TMA ? 8 : 2;   // units of this warp (the element loader's CTAs have BN <= 64)
                 float v[NU][16];
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[i][j] = 0.0f;
-                for (int k0 = 0; k0 < nkb; k0 += p.promote, ++acc) {
+                    for (int k = 0; k < 16; ++k) v[i][k] = 0.0f;
+                for (int k0 = 0; k0 < nkb; k0 += kLtPromote, ++acc) {
                     const int ab = acc & 1;
                     take(ab);
 #pragma unroll
                     for (int i = 0; i < NU; ++i) {
                         if (uh + 2 * i < units) {
-                            float x[16];
-                            ld16(tmem + lane_addr + ab * BN + (uh + 2 * i) * 16, x);
+                            uint32_t r[16];
+                            tmem_ld16(tmem + lane_addr + ab * BN + (uh + 2 * i) * 16, r);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) v[i][j] += x[j];
+                            for (int k = 0; k < 16; ++k) v[i][k] += __uint_as_float(r[k]);
                         }
                     }
                     release(ab);
                 }
+                units_do([&](int, float (&x)[16]) {   // the units in turn through v[0]: one copy of the code above
 #pragma unroll
-                for (int i = 0; i < NU; ++i)
-                    if (uh + 2 * i < units) done(uh + 2 * i, v[i]);
+                    for (int k = 0; k < 16; ++k) x[k] = v[0][k];
+#pragma unroll
+                    for (int i = 0; i + 1 < NU; ++i)
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[i][k] = v[i + 1][k];
+                });
             }
             if (split > 1) {
                 lt_cluster_fence();
@@ -869,18 +1074,21 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 if (lane < split) lt_arrive_remote(lt_map(red_full, static_cast<uint32_t>(lane)));
                 if (!lt_poll<16>(red_full, parts & 1, abort_flag, a.timeout_ns) && lane == 0)
                     latch_error(a.err, ERR_ETIMEOUT, parts, KID_LINEAR);
-                // items of four rows x one lane group over all warps of the cluster
-                for (int it = rank * kLtEpiWarps + warp - 4; it < (t.nrows + 3) / 4 * 4; it += split * kLtEpiWarps) {
-                    const int lg = it & 3, first = it >> 2 << 2;
+                lt_cluster_fence();
+                const int items = (t.nrows + 3) / 4 * 4;
+                for (int at = warp - 4, it = rank * kLtEpiWarps + warp - 4; it < items;
+                     at += kLtEpiWarps, it += split * kLtEpiWarps) {
                     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    const float* at = red + first * kLtM + 32 * lg + lane;
-                    for (int s = 0; s < split; ++s) {
-                        const uint32_t from = lt_map(at, static_cast<uint32_t>(s));
+                    const float* from = red + at * split * 128 + lane;
+                    for (int s = 0; s < split; ++s)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] += lt_ld_cluster(from + j * kLtM * 4);
-                    }
-                    finish(t, lg, first, v);
+                        for (int j = 0; j < 4; ++j) v[j] += from[s * 128 + j * 32];
+                    const int first = it >> 2 << 2, ci = col(t, it & 3), orow = rows_of(t, first, 4);
+                    uint32_t raw[4 / RS];
+                    residual(t, ci, first, orow, raw);
+                    finish(t, ci, first, orow, bias_of(t, 0, ci), DUAL ? bias_of(t, 1, ci) : 0.0f, v, raw);
                 }
+                lt_cluster_fence();
                 __syncwarp();
                 if (lane < split) lt_arrive_remote(lt_map(red_empty, static_cast<uint32_t>(lane)));
                 ++parts;
@@ -902,9 +1110,9 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
 }
 
 // ------------------------------------------------------------------ host side
-// 16-bit tensor map with a 128-byte swizzle: up to three dimensions, innermost contiguous.
-inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
-                      uint64_t s2, uint32_t b1) {
+// 16-bit tensor map with a 128-byte swizzle, innermost dimension contiguous; strides in elements.
+inline bool lt_encode_n(CUtensorMap* map, int type, const void* base, int rank, const cuuint64_t* dims,
+                        const cuuint64_t* strides, uint32_t rows) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     if (!encode) {
         cudaDriverEntryPointQueryResult q;
@@ -914,13 +1122,25 @@ inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0,
             return false;
         encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     }
-    const cuuint64_t dims[3] = {d0, d1, d2};
-    const cuuint64_t strides[2] = {s1 * 2, s2 * 2};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kLtBK), b1, 1}, es[3] = {1, 1, 1};
+    const cuuint64_t bytes[2] = {strides[0] * 2, rank > 2 ? strides[1] * 2 : 0};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kLtBK), rows, 1}, es[3] = {1, 1, 1};
     return encode(map, type == LIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                  3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, bytes, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Boxes of 64 x `rows` of a stack of matrices.
+inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+                      uint64_t s2, uint32_t rows) {
+    const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1, s2};
+    return lt_encode_n(map, type, base, 3, dims, strides, rows);
+}
+
+// Single rows of 64 values, for gathers.
+inline bool lt_encode2(CUtensorMap* map, int type, const void* base, uint64_t d0, uint64_t d1, uint64_t s1) {
+    const cuuint64_t dims[2] = {d0, d1}, strides[1] = {s1};
+    return lt_encode_n(map, type, base, 2, dims, strides, 1);
 }
 
 // Whether TMA can read the operands as they lie: 16-byte aligned bases, strides of whole 16 bytes.
@@ -932,7 +1152,8 @@ inline bool lt_tma_ok(const LinArgs& a) {
 }
 
 // One candidate tile shape and what it is estimated to take, in SM cycles.
-inline double lt_shape(const LinArgs& a, bool tma, int cg, int split, int bn, int sm_count, int smem_limit, LtPlan* p) {
+inline double lt_shape(const LinArgs& a, bool tma, int cg, int split, int bn, const int* slots_of, int smem_limit,
+                       LtPlan* p) {
     const bool dual = a.kind == LIN_FWD && a.a[1], wg = a.kind == LIN_WGRAD;
     *p = LtPlan{};
     p->bn = bn;
@@ -940,12 +1161,12 @@ inline double lt_shape(const LinArgs& a, bool tma, int cg, int split, int bn, in
     p->split = split;
     p->ct = dual ? kLtM / 2 : kLtM;
     p->n_ct = (a.C + p->ct * cg - 1) / (p->ct * cg);
-    p->promote = a.out_type == LIN_F32 ? kLtPromote : 0;
     const int brows = bn / cg;
     p->bbox = brows < 64 ? brows : 64;
     p->stage_bytes = kLtATile + ((wg ? (brows + 63) / 64 * 64 : brows) * 128 + 1023) / 1024 * 1024;
     p->off_ring = (kLtOffPrefix + 4 * (a.E + 1) + 1023) / 1024 * 1024;
-    const int red = split > 1 ? bn * kLtM * 4 : 0;
+    // items: bn / 4 quarters x 4 lane groups, in rounds of all the cluster's warps
+    const int red = split > 1 ? (bn + kLtEpiWarps * split - 1) / (kLtEpiWarps * split) * kLtEpiWarps * split * 512 : 0;
     p->stages = (smem_limit - 1024 - p->off_ring - red) / p->stage_bytes;
     if (p->stages > kLtMaxStages) p->stages = kLtMaxStages;
     p->off_red = p->off_ring + p->stages * p->stage_bytes;
@@ -973,37 +1194,39 @@ inline double lt_shape(const LinArgs& a, bool tma, int cg, int split, int bn, in
     }
     if (fill > 1) fill = 1;
     if (most > (1 << 30) || p->stages < 3) return -1;
-    const int slots = sm_count / cl;                  // clusters at a time
+    const int slots = slots_of[cl];                   // clusters at a time
     p->grid = static_cast<int>(most < slots ? most : slots) * cl;
-    // a stage: the MMAs (two cycles a column) or its bytes from L2 (~42 a cycle and SM with all of them reading)
-    const double busy = tiles * cl < sm_count ? tiles * cl / sm_count : 1.0;
-    double bytes = kLtATile + brows * 128 * fill;
-    double stage = 2.0 * bn * fill > bytes / (42 / (0.3 + 0.7 * busy)) ? 2.0 * bn * fill
-                                                                        : bytes / (42 / (0.3 + 0.7 * busy));
+    // A stage: the MMAs (two cycles a column), its bytes into shared memory (48 a cycle measured, from L2) or, for a
+    // small one, what the hand-offs of the ring cost.
+    const double bytes = kLtATile + brows * 128 * fill;
+    double stage = 2.0 * bn * fill;
+    if (stage < bytes / 48) stage = bytes / 48;
+    if (stage < (dual ? 560 : 480)) stage = dual ? 560 : 480;
     if (!tma) stage = (kLtM + brows * fill) * 16;     // element by element
-    if (stage < 150) stage = 150;
     const double rounds = a.E == 1 || wg ? static_cast<double>((static_cast<long long>(tiles) + slots - 1) / slots)
                                          : (tiles / slots > 1 ? tiles / slots + 0.5 : 1.0);
     const double tile = nkb / split * stage, out = 12.0 * bn * fill;   // out: the epilogue, hidden but for the last
-    return rounds * (tile > out ? tile : out) + out / (split > 1 ? 2 : 1) + (split > 1 ? 2500 + 150 * split : 0) +
+    return rounds * (tile > out ? tile : out) + out / (split > 1 ? 2 : 1) + (split > 1 ? 3000 + 100 * split : 0) +
            (cg > 1 ? 500 : 0);
 }
 
-// The shape with the smallest estimate.
-inline LtPlan lt_plan(const LinArgs& a, bool tma, int sm_count, int smem_limit) {
+// The shape with the smallest estimate.  slots: how many clusters of n CTAs the GPU holds at a time, n = 1 .. 8.
+inline LtPlan lt_plan(const LinArgs& a, bool tma, const int* slots, int smem_limit) {
     LtPlan best{}, p;
     double least = -1;
     const int nkb = a.kind == LIN_WGRAD ? (a.rows / a.E + kLtBK - 1) / kLtBK
                                         : (a.Q + kLtBK - 1) / kLtBK * (a.kind == LIN_DGRAD && a.b[1] ? 2 : 1);
-    const int most = tma || a.out_type != LIN_F32 ? 256 : 128;
+    const int most = tma || a.out_type != LIN_F32 ? 256 : 64;
     for (int cg = 1; cg <= (tma ? 2 : 1); ++cg)
         for (int bn = (a.kind == LIN_WGRAD ? 64 : 16) * cg; bn <= most; bn *= 2)
-            for (int split = 1; split <= (cg == 1 ? 8 : 1) && (split == 1 || split * 4 <= nkb); ++split) {
-                const double t = lt_shape(a, tma, cg, split, bn, sm_count, smem_limit, &p);
-                if (t >= 0 && (least < 0 || t < least)) {
+            for (int split = 1; split <= 8 && (split == 1 || (cg == 1 && split * 4 <= nkb)); ++split) {
+                const double t = lt_shape(a, tma, cg, split, bn, slots, smem_limit, &p);
+                if (t < 0) continue;
+                if (least < 0 || t < least) {
                     least = t;
                     best = p;
                 }
+                if (p.grid == slots[cg * split] * cg * split) break;   // the GPU is full: no finer split helps
             }
     return best;
 }
@@ -1015,7 +1238,7 @@ inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     bool ok = true;
     if (a.kind == LIN_WGRAD) {   // A = x [rows, C], B = dz [rows, out_n]
         const uint64_t xr = g ? a.gather_total : R;
-        ok = lt_encode(&m->a0, a.type, a.a[0], C, xr, 1, lda, lda * xr, 64) &&
+        ok = (g ? lt_encode2(&m->a0, a.type, a.a[0], C, xr, lda) : lt_encode(&m->a0, a.type, a.a[0], C, xr, 1, lda, lda * xr, 64)) &&
              lt_encode(&m->b0, a.type, a.b[0], a.out_n, R, 1, ldb, ldb * R, 64);
         m->a1 = m->a0;
         m->b1 = m->b0;
@@ -1027,7 +1250,8 @@ inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     const uint64_t br = g && fwd ? a.gather_total : R;
     const uint32_t abox = !fwd ? 64 : a.a[1] ? 16 : kLtM;
     ok = lt_encode(&m->a0, a.type, a.a[0], inner, outer, E, lda, gs, abox) &&
-         lt_encode(&m->b0, a.type, a.b[0], Q, br, 1, ldb, ldb * br, p.bbox);
+         (g && fwd ? lt_encode2(&m->b0, a.type, a.b[0], Q, br, ldb)
+                   : lt_encode(&m->b0, a.type, a.b[0], Q, br, 1, ldb, ldb * br, p.bbox));
     m->a1 = m->a0;
     m->b1 = m->b0;
     if (a.a[1]) ok = ok && lt_encode(&m->a1, a.type, a.a[1], inner, outer, E, lda, gs, abox);
@@ -1035,17 +1259,21 @@ inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     return ok;
 }
 
-// Launch the kernel a plan asks for (one translation unit per direction: linear_fwd.cu, linear_dgrad.cu,
+// Launch the kernel a plan asks for (a translation unit each: linear_fwd.cu, linear_swiglu.cu, linear_dgrad.cu,
 // linear_wgrad.cu).
 cudaError_t lin_launch_fwd(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
+cudaError_t lin_launch_swiglu(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
 cudaError_t lin_launch_dgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
 cudaError_t lin_launch_wgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
 // Let the kernels of a direction use `bytes` of dynamic shared memory on the current device.
 cudaError_t lin_allow_fwd(int bytes);
+cudaError_t lin_allow_swiglu(int bytes);
 cudaError_t lin_allow_dgrad(int bytes);
 cudaError_t lin_allow_wgrad(int bytes);
+// How many clusters of n = 1 .. 8 CTAs of these kernels the current device holds at a time (slots[0] unused).
+cudaError_t lin_slots(int smem, int* slots);
 
-template <int KIND, bool DUAL, bool TMA, int CG>
+template <int KIND, bool DUAL, bool TMA, int CG, bool SPANS>
 cudaError_t lt_launch_k(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
@@ -1061,20 +1289,30 @@ cudaError_t lt_launch_k(const LinArgs& a, const LtPlan& p, const LtMaps& m, cuda
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cg * p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, lin_tc_kernel<KIND, DUAL, TMA, CG>, a, p, m);
+    return cudaLaunchKernelEx(&cfg, lin_tc_kernel<KIND, DUAL, TMA, CG, SPANS>, a, p, m);
+}
+
+template <int KIND, bool DUAL, bool SPANS>
+cudaError_t lt_launch(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
+    if (!tma) return lt_launch_k<KIND, DUAL, false, 1, SPANS>(a, p, m, s);
+    return p.cg == 2 ? lt_launch_k<KIND, DUAL, true, 2, SPANS>(a, p, m, s)
+                     : lt_launch_k<KIND, DUAL, true, 1, SPANS>(a, p, m, s);
 }
 
 template <int KIND, bool DUAL>
 cudaError_t lt_launch(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
-    if (!tma) return lt_launch_k<KIND, DUAL, false, 1>(a, p, m, s);
-    return p.cg == 2 ? lt_launch_k<KIND, DUAL, true, 2>(a, p, m, s) : lt_launch_k<KIND, DUAL, true, 1>(a, p, m, s);
+    return a.out_type == LIN_F32 ? lt_launch<KIND, DUAL, true>(a, p, m, tma, s)
+                                 : lt_launch<KIND, DUAL, false>(a, p, m, tma, s);
 }
 
 template <int KIND, bool DUAL>
 cudaError_t lt_allow(int bytes) {
-    const void* k[] = {reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 1>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 2>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, false, 1>)};
+    const void* k[] = {reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 1, false>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 2, false>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, false, 1, false>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 1, true>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 2, true>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, false, 1, true>)};
     for (const void* f : k) {
         const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;

@@ -51,6 +51,7 @@ struct moe_fp4_ctx {
     std::vector<int64_t> slot_owner;   // slot -> layer*E+expert or -1
     int path = MOE_FP4_PATH_AUTO;
     int smem_optin = 0;                // opt-in shared memory per block (bytes)
+    int lin_slots[9] = {};             // clusters of 1 .. 8 CTAs of the 16-bit products the device holds at a time
     bool profile = false;
     struct ProfRec { const char* name; cudaEvent_t a, b; };
     std::vector<ProfRec> prof;         // profiled launches not yet read
@@ -432,7 +433,9 @@ moe_fp4_status moe_fp4_create(const moe_fp4_config* cfg, int device, void* arena
     }
     mx_bind(&c->mx, c->d_mx, mo, mz.cnt);
     if (allow_mx_smem(c->smem_optin) != cudaSuccess || lin_allow_fwd(c->smem_optin) != cudaSuccess ||
+        lin_allow_swiglu(c->smem_optin) != cudaSuccess ||
         lin_allow_dgrad(c->smem_optin) != cudaSuccess || lin_allow_wgrad(c->smem_optin) != cudaSuccess ||
+        lin_slots(c->smem_optin, c->lin_slots) != cudaSuccess ||
         cudaMemset(c->d_mx, 0, mo.xp) != cudaSuccess) {   // sequence, counters, flags, zero block
         cudaGetLastError();
         return bail(MOE_FP4_ECUDA);
@@ -922,7 +925,7 @@ int64_t lin_gs(int64_t gs, int64_t rows, int64_t ld, int64_t width) {
 
 cudaError_t lin_run(moe_fp4_ctx* c, const char* name, const LinArgs& a, cudaStream_t s) {
     const bool tma = lt_tma_ok(a);
-    const LtPlan p = lt_plan(a, tma, c->sm_count, c->smem_optin);
+    const LtPlan p = lt_plan(a, tma, c->lin_slots, c->smem_optin);
     if (p.grid < 1) return cudaErrorInvalidConfiguration;
     LtMaps m{};
     if (tma && !lt_maps(a, p, &m)) return cudaErrorInvalidValue;
@@ -933,9 +936,10 @@ cudaError_t lin_run(moe_fp4_ctx* c, const char* name, const LinArgs& a, cudaStre
         eb = take_event(c);
         cudaEventRecord(ea, s);
     }
-    const cudaError_t e = a.kind == LIN_FWD     ? lin_launch_fwd(a, p, m, tma, s)
-                          : a.kind == LIN_DGRAD ? lin_launch_dgrad(a, p, m, tma, s)
-                                                : lin_launch_wgrad(a, p, m, tma, s);
+    const cudaError_t e = a.kind == LIN_DGRAD   ? lin_launch_dgrad(a, p, m, tma, s)
+                          : a.kind == LIN_WGRAD ? lin_launch_wgrad(a, p, m, tma, s)
+                          : a.a[1]              ? lin_launch_swiglu(a, p, m, tma, s)
+                                                : lin_launch_fwd(a, p, m, tma, s);
     if (prof) {
         cudaEventRecord(eb, s);
         c->prof.push_back({name, ea, eb});

@@ -6,7 +6,6 @@ when the library is missing; there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -32,6 +31,9 @@ EXPORTS = ("moe_fp4_slot_bytes", "moe_fp4_create", "moe_fp4_destroy", "moe_fp4_a
 # element types and activations of the 16-bit products (moe_fp4_linear)
 BF16, F16, F32 = 0, 1, 2
 _TYPES = {torch.bfloat16: BF16, torch.int16: BF16, torch.uint16: BF16, torch.float16: F16, torch.float32: F32}
+# the float type of a tensor that may hold bf16 bits
+_PLAIN = {torch.bfloat16: torch.bfloat16, torch.int16: torch.bfloat16, torch.uint16: torch.bfloat16,
+          torch.float16: torch.float16}
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 
 
@@ -422,42 +424,61 @@ class Context:
                 stream):
         chk = _Check(self, what)
         E, N, K, wdt = chk.weights(w, offsets, w_up)
-        R = chk.rows(x, x_rows, K, wdt)
-        lead = () if offsets is None else (E,)
-        y_total = R if y_rows is None else (y.shape[0] if y is not None else
-                                            (residual.shape[0] if residual is not None else R))
         act_id = chk.act(act, w_up)
-        a = LinearArgs(rows=R, in_features=K, out_features=N, type=wdt, act=act_id,
-                       n_groups=0 if offsets is None else E, x_total=x.shape[0], y_total=y_total)
-        a.offsets, a.x_rows, a.y_rows = _addr(offsets), chk.index(x_rows, "x_rows", R), chk.index(y_rows, "y_rows", R)
-        a.x, a.ldx = chk.matrix(x, "x", (x.shape[0], K), (wdt,))
-        a.w, a.ldw, a.w_group_stride = chk.weight_layout(w)
+        px, ldx, x_total = chk.rows(x, K, wdt)
+        R = x_total if x_rows is None else chk.length(x_rows, "x_rows")
+        lead = (N,) if offsets is None else (E, N)
+        if y_rows is None:
+            y_total = R
+        elif y is not None:
+            y_total = y.shape[0]
+        else:
+            y_total = R if residual is None else residual.shape[0]
+        pw, ldw, gs = chk.layout(w, "w", w.shape)
+        pu = None
         if w_up is not None:
-            if chk.weight_layout(w_up)[1:] != (a.ldw, a.w_group_stride):
+            pu, ld_up, gs_up = chk.layout(w_up, "w_up", w.shape)
+            if (ld_up, gs_up) != (ldw, gs):
                 chk.fail("w and w_up differ in their strides")
-            a.w_up = w_up.data_ptr()
-        for t, name in ((bias, "bias"), (bias_up, "bias_up")):
-            if t is not None:
-                setattr(a, name, chk.dense(t, name, lead + (N,)))
-                if bias is not None and t.dtype != bias.dtype:
-                    chk.fail("bias and bias_up differ in type")
-                a.bias_type = _TYPES[t.dtype]
+        pb = pbu = pr = None
+        bt = rt = ldr = 0
+        if bias is not None:
+            pb, bt = chk.dense(bias, "bias", lead), _TYPES[bias.dtype]
+        if bias_up is not None:
+            if w_up is None:
+                chk.fail("bias_up goes with w_up")
+            pbu = chk.dense(bias_up, "bias_up", lead)
+            if bias is not None and bias.dtype != bias_up.dtype:
+                chk.fail("bias and bias_up differ in type")
+            bt = _TYPES[bias_up.dtype]
         if residual is not None:
-            a.residual, a.ld_residual = chk.matrix(residual, "residual", (y_total, N))
-            a.residual_type = _TYPES[residual.dtype]
-        with chk.on(stream) as s:
-            if y is None:
-                y = torch.empty((y_total, N), dtype=out_dtype or chk.plain(x.dtype), device=x.device)
-            a.y, a.ldy = chk.matrix(y, "y", (y_total, N))
-            a.y_type = _TYPES[y.dtype]
+            pr, ldr = chk.matrix(residual, "residual", y_total, N)
+            rt = _TYPES[residual.dtype]
+        pxr = None if x_rows is None else chk.index(x_rows, "x_rows", R)
+        pyr = None if y_rows is None else chk.index(y_rows, "y_rows", R)
+
+        def call(s, other, y):
             z = z_up = None
+            if y is None:
+                y = torch.empty((y_total, N), dtype=out_dtype or _PLAIN[x.dtype], device=x.device)
+            elif out_dtype is not None and out_dtype != y.dtype:
+                chk.fail("y and out_dtype differ")
+            py, ldy = chk.matrix(y, "y", y_total, N)
             if save:
-                z = torch.empty((R, N), dtype=chk.plain(x.dtype), device=x.device)
+                z = torch.empty((R, N), dtype=_PLAIN[x.dtype], device=x.device)
                 z_up = torch.empty_like(z) if w_up is not None else None
-                a.z, a.z_up, a.ldz = _addr(z), _addr(z_up), N
-            chk.keep(s, x, w, w_up, offsets, bias, bias_up, residual, x_rows, y_rows, y, z, z_up)
-            self._check(self.lib.moe_fp4_linear(self.h, ctypes.byref(a), ctypes.c_void_p(s.cuda_stream)), what)
-        return (y, z, z_up) if save else y
+            a = LinearArgs(R, K, N, wdt, act_id, 0 if offsets is None else E,
+                           None if offsets is None else offsets.data_ptr(), pxr, pyr, x_total, y_total, px, pw, pu,
+                           ldx, ldw, gs, pb, pbu, bt, rt, pr, ldr, py, ldy, _TYPES[y.dtype], 0,
+                           None if z is None else z.data_ptr(), None if z_up is None else z_up.data_ptr(), N)
+            if other is not None:
+                chk.keep(other, x, w, w_up, offsets, bias, bias_up, residual, x_rows, y_rows, y, z, z_up)
+            rc = self.lib.moe_fp4_linear(self.h, ctypes.byref(a), s)
+            if rc != OK:
+                self._check(rc, what)
+            return (y, z, z_up) if save else y
+
+        return chk.run(stream, call, y)
 
     def linear_backward(self, dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, w_up: torch.Tensor | None = None,
                         z: torch.Tensor | None = None, z_up: torch.Tensor | None = None, act: str = "none",
@@ -501,154 +522,162 @@ class Context:
                          db, db_up, dw_dtype, accumulate, x_rows, y_rows, dx_rows, stream) -> LinearGrads:
         chk = _Check(self, what)
         E, N, K, wdt = chk.weights(w, offsets, w_up)
-        R = chk.rows(x, x_rows, K, wdt)
-        lead = () if offsets is None else (E,)
-        two = w_up is not None
         act_id = chk.act(act, w_up)
+        two = w_up is not None
+        px, ldx, x_total = chk.rows(x, K, wdt)
+        R = x_total if x_rows is None else chk.length(x_rows, "x_rows")
+        lead = (N,) if offsets is None else (E, N)
         if act_id and z is None or two and z_up is None:
             chk.fail("z (and z_up) of the forward pass are needed")
-        if not two and any(t is not None for t in (z_up, dw_up, db_up)):
+        if not two and not (z_up is None and dw_up is None and db_up is None):
             chk.fail("z_up, dw_up and db_up go with w_up")
-        if (not need_dx and dx is not None) or (not need_dw and (dw is not None or dw_up is not None)) or \
-                (not need_db and (db is not None or db_up is not None)):
+        if (not need_dx and dx is not None) or (not need_dw and not (dw is None and dw_up is None)) or \
+                (not need_db and not (db is None and db_up is None)):
             chk.fail("an output was given for a gradient that is not needed")
         if accumulate and ((need_dw and (dw is None or two and dw_up is None)) or
                            (need_db and (db is None or two and db_up is None))):
             chk.fail("accumulate adds to given outputs")
         dy_total = R if y_rows is None else dy.shape[0]
-        dx_total = R if dx_rows is None else (dx.shape[0] if dx is not None else R)
-        a = LinearGradArgs(rows=R, in_features=K, out_features=N, type=wdt, act=act_id,
-                           n_groups=0 if offsets is None else E, x_total=x.shape[0], y_total=dy_total,
-                           dx_total=dx_total, accumulate=int(accumulate))
-        a.offsets, a.x_rows = _addr(offsets), chk.index(x_rows, "x_rows", R)
-        a.y_rows, a.dx_rows = chk.index(y_rows, "y_rows", R), chk.index(dx_rows, "dx_rows", R)
-        a.dy, a.lddy = chk.matrix(dy, "dy", (dy_total, N), (wdt, F32))
-        a.dy_type = _TYPES[dy.dtype]
-        a.x, a.ldx = chk.matrix(x, "x", (x.shape[0], K), (wdt,))
-        a.w, a.ldw, a.w_group_stride = chk.weight_layout(w)
+        dx_total = R if dx_rows is None or dx is None else dx.shape[0]
+        pdy, lddy = chk.matrix(dy, "dy", dy_total, N, (wdt, F32))
+        dyt = _TYPES[dy.dtype]
+        pw, ldw, gs = chk.layout(w, "w", w.shape)
+        pu = pz = pzu = None
+        ldz = 0
         if two:
-            if chk.weight_layout(w_up)[1:] != (a.ldw, a.w_group_stride):
+            pu, ld_up, gs_up = chk.layout(w_up, "w_up", w.shape)
+            if (ld_up, gs_up) != (ldw, gs):
                 chk.fail("w and w_up differ in their strides")
-            a.w_up = w_up.data_ptr()
         if act_id:
-            a.z, a.ldz = chk.matrix(z, "z", (R, N), (wdt,))
+            pz, ldz = chk.matrix(z, "z", R, N, (wdt,))
             if two:
-                a.z_up, ld_up = chk.matrix(z_up, "z_up", (R, N), (wdt,))
-                if ld_up != a.ldz:
+                pzu, ld_up = chk.matrix(z_up, "z_up", R, N, (wdt,))
+                if ld_up != ldz:
                     chk.fail("z and z_up differ in their strides")
-        t16 = chk.plain(x.dtype)
-        with chk.on(stream) as s:
+        pxr = None if x_rows is None else chk.index(x_rows, "x_rows", R)
+        pyr = None if y_rows is None else chk.index(y_rows, "y_rows", R)
+        pdr = None if dx_rows is None else chk.index(dx_rows, "dx_rows", R)
+        t16 = _PLAIN[x.dtype]
+        need_dz = (act_id != 0 or dyt == F32 or y_rows is not None) and (need_dx or need_dw)
+
+        def call(s, other, dx, dw, dw_up, db, db_up):
             def new(shape, dtype):
                 return torch.empty(shape, dtype=dtype, device=x.device)
 
-            dz = dz_up = None
-            if (act_id or _TYPES[dy.dtype] == F32 or y_rows is not None) and (need_dx or need_dw):
-                dz = new((R, N), t16)
-                dz_up = new((R, N), t16) if two else None
-                a.dz, a.dz_up, a.lddz = _addr(dz), _addr(dz_up), N
+            pdx = pdw = pdwu = pdb = pdbu = None
+            lddx = lddw = dgs = dxt = dwt = 0
+            dz = new((R, N), t16) if need_dz else None
+            dz_up = new((R, N), t16) if need_dz and two else None
             if need_dx:
                 dx = new((dx_total, K), t16) if dx is None else dx
-                a.dx, a.lddx = chk.matrix(dx, "dx", (dx_total, K))
-                a.dx_type = _TYPES[dx.dtype]
+                pdx, lddx = chk.matrix(dx, "dx", dx_total, K)
+                dxt = _TYPES[dx.dtype]
             if need_dw:
-                dw = new(lead + (N, K), dw_dtype or t16) if dw is None else dw
-                a.dw, a.lddw, a.dw_group_stride = chk.grad_layout(dw, "dw", lead + (N, K))
-                a.dw_type = _TYPES[dw.dtype]
+                if dw is None:
+                    dw = new(lead + (K,), dw_dtype or (t16 if dw_up is None else dw_up.dtype))
+                pdw, lddw, dgs = chk.layout(dw, "dw", lead + (K,))
+                dwt = _TYPES[dw.dtype]
+                if dw_dtype is not None and _TYPES.get(dw_dtype) != dwt:
+                    chk.fail("dw and dw_dtype differ")
                 if two:
-                    dw_up = torch.empty_like(dw) if dw_up is None else dw_up
-                    if dw_up.dtype != dw.dtype or \
-                            chk.grad_layout(dw_up, "dw_up", lead + (N, K))[1:] != (a.lddw, a.dw_group_stride):
+                    dw_up = torch.empty_strided(dw.shape, dw.stride(), dtype=dw.dtype, device=x.device) \
+                        if dw_up is None else dw_up
+                    pdwu, ld_up, gs_up = chk.layout(dw_up, "dw_up", lead + (K,))
+                    if _TYPES[dw_up.dtype] != dwt or (ld_up, gs_up) != (lddw, dgs):
                         chk.fail("dw and dw_up differ in type or strides")
-                    a.dw_up = dw_up.data_ptr()
             if need_db:
-                db = new(lead + (N,), torch.float32) if db is None else db
-                a.db = chk.dense(db, "db", lead + (N,), (F32,))
+                db = new(lead, torch.float32) if db is None else db
+                pdb = chk.dense(db, "db", lead, (F32,))
                 if two:
                     db_up = torch.empty_like(db) if db_up is None else db_up
-                    a.db_up = chk.dense(db_up, "db_up", lead + (N,), (F32,))
-            chk.keep(s, dy, x, w, w_up, offsets, z, z_up, x_rows, y_rows, dx_rows, dz, dz_up, dx, dw, dw_up, db,
-                     db_up)
-            self._check(self.lib.moe_fp4_linear_backward(self.h, ctypes.byref(a), ctypes.c_void_p(s.cuda_stream)),
-                        what)
-        return LinearGrads(dx, dw, dw_up, db, db_up)
+                    pdbu = chk.dense(db_up, "db_up", lead, (F32,))
+            a = LinearGradArgs(R, K, N, wdt, act_id, 0 if offsets is None else E,
+                               None if offsets is None else offsets.data_ptr(), pxr, pyr, pdr, x_total, dy_total,
+                               dx_total, dyt, pdy, lddy, pz, pzu, ldz, px, pw, pu, ldx, ldw, gs,
+                               None if dz is None else dz.data_ptr(), None if dz_up is None else dz_up.data_ptr(), N,
+                               pdx, lddx, dxt, dwt, pdw, pdwu, lddw, dgs, pdb, pdbu, int(accumulate), 0)
+            if other is not None:
+                chk.keep(other, dy, x, w, w_up, offsets, z, z_up, x_rows, y_rows, dx_rows, dz, dz_up, dx, dw, dw_up, db,
+                         db_up)
+            rc = self.lib.moe_fp4_linear_backward(self.h, ctypes.byref(a), s)
+            if rc != OK:
+                self._check(rc, what)
+            return LinearGrads(dx, dw, dw_up, db, db_up)
 
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+        return chk.run(stream, call, dx, dw, dw_up, db, db_up)
 
 
 class _Check:
     """Argument checks of the 16-bit products: what the C call cannot see (devices, shapes, tensor types)."""
+    __slots__ = ("ctx", "dev", "what")
 
     def __init__(self, ctx: Context, what: str):
-        self.ctx, self.what = ctx, what
+        self.ctx, self.dev, self.what = ctx, ctx.device, what
 
     def fail(self, why: str):
         raise MoeError(EINVAL, f"{self.what}: {why}")
 
-    def tensor(self, t, name: str, types=(BF16, F16, F32)):
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.device.index != self.ctx.device:
-            self.fail(f"{name} is not a tensor on the context's device {self.ctx.device}")
-        if t.dtype not in _TYPES or _TYPES[t.dtype] not in types:
+    def tensor(self, t, name: str, types):
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.dev:
+            self.fail(f"{name} is not a tensor on the context's device {self.dev}")
+        if _TYPES.get(t.dtype, -1) not in types:
             self.fail(f"{name} has type {t.dtype}")
 
-    def matrix(self, t, name: str, shape, types=(BF16, F16, F32)):
+    def matrix(self, t, name: str, rows: int, cols: int, types=(BF16, F16, F32)):
         """(address, row stride) of a 2-D tensor with contiguous rows."""
         self.tensor(t, name, types)
-        if tuple(t.shape) != tuple(shape):
-            self.fail(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        if t.shape[1] > 1 and t.stride(1) != 1:
+        if tuple(t.shape) != (rows, cols):
+            self.fail(f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
+        ld, inner = t.stride()
+        if inner != 1 and cols > 1:
             self.fail(f"{name} needs a contiguous last dimension")
-        ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-        if ld < t.shape[1]:
+        if rows < 2:
+            ld = cols
+        elif ld < cols:
             self.fail(f"{name}'s rows overlap")
         return t.data_ptr(), ld
 
+    def rows(self, x, K: int, wdt: int):
+        """(address, row stride, rows) of x."""
+        self.tensor(x, "x", (wdt,))
+        if x.dim() != 2 or x.shape[1] != K:
+            self.fail(f"x has shape {tuple(x.shape)}, not [rows, {K}]")
+        n = x.shape[0]
+        return *self.matrix(x, "x", n, K, (wdt,)), n
+
     def dense(self, t, name: str, shape, types=(BF16, F16, F32)):
         self.tensor(t, name, types)
-        if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-            self.fail(f"{name} has to be a contiguous tensor of shape {tuple(shape)}")
+        if tuple(t.shape) != shape or not t.is_contiguous():
+            self.fail(f"{name} has to be a contiguous tensor of shape {shape}")
         return t.data_ptr()
 
-    def grad_layout(self, t, name: str, shape, types=(BF16, F16, F32)):
+    def layout(self, t, name: str, shape, types=(BF16, F16, F32)):
         """(address, row stride, group stride) of [N, K] or [E, N, K] with contiguous rows."""
         self.tensor(t, name, types)
         if tuple(t.shape) != tuple(shape):
             self.fail(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        if shape[-1] > 1 and t.stride(-1) != 1:
+        st, n, k = t.stride(), shape[-2], shape[-1]
+        ld = st[-2] if n > 1 else k
+        gs = st[0] if len(shape) == 3 and shape[0] > 1 else n * ld
+        if k > 1 and st[-1] != 1:
             self.fail(f"{name} needs a contiguous last dimension")
-        ld = t.stride(-2) if shape[-2] > 1 else shape[-1]
-        gs = t.stride(0) if len(shape) == 3 and shape[0] > 1 else shape[-2] * ld
-        if ld < shape[-1] or (len(shape) == 3 and gs < (shape[-2] - 1) * ld + shape[-1]):
+        if ld < k or gs < (n - 1) * ld + k:
             self.fail(f"{name}'s rows overlap")
         return t.data_ptr(), ld, gs
-
-    def weight_layout(self, w):
-        return self.grad_layout(w, "w", tuple(w.shape))
 
     def weights(self, w, offsets, w_up):
         self.tensor(w, "w", (BF16, F16))
         want = 2 if offsets is None else 3
-        if w.dim() != want or min(w.shape) < 1:
+        if w.dim() != want or w.numel() == 0:
             self.fail(f"w has shape {tuple(w.shape)}, not {want} dimensions of one or more")
+        wdt = _TYPES[w.dtype]
         if w_up is not None:
-            self.tensor(w_up, "w_up", (_TYPES[w.dtype],))
-            if w_up.shape != w.shape:
-                self.fail("w and w_up differ in shape")
+            self.tensor(w_up, "w_up", (wdt,))
         E = 1
         if offsets is not None:
             E = w.shape[0]
-            if not isinstance(offsets, torch.Tensor) or offsets.dtype != torch.int32 or \
-                    tuple(offsets.shape) != (E + 1,) or not offsets.is_contiguous() or \
-                    offsets.device != w.device:
-                self.fail(f"offsets has to be a contiguous int32 [{E + 1}] on w's device")
-        return E, w.shape[-2], w.shape[-1], _TYPES[w.dtype]
-
-    def rows(self, x, x_rows, K, wdt):
-        self.tensor(x, "x", (wdt,))
-        if x.dim() != 2 or x.shape[1] != K:
-            self.fail(f"x has shape {tuple(x.shape)}, not [rows, {K}]")
-        return x.shape[0] if x_rows is None else x_rows.numel()
+            self.index(offsets, "offsets", E + 1)
+        return E, w.shape[-2], w.shape[-1], wdt
 
     def act(self, act, w_up):
         if act not in ACTS:
@@ -657,36 +686,45 @@ class _Check:
             self.fail("w_up goes with act='swiglu'")
         return ACTS[act]
 
+    def length(self, t, name: str):
+        if not isinstance(t, torch.Tensor) or t.dim() != 1:
+            self.fail(f"{name} has to be a contiguous int32 vector on the context's device")
+        return t.shape[0]
+
     def index(self, t, name: str, n: int):
-        if t is None:
-            return None
         if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or tuple(t.shape) != (n,) or \
-                not t.is_contiguous() or t.device.type != "cuda" or t.device.index != self.ctx.device:
+                not t.is_contiguous() or t.get_device() != self.dev:
             self.fail(f"{name} has to be a contiguous int32 [{n}] on the context's device")
         return t.data_ptr()
 
+    def run(self, stream, call, *outputs):
+        """call(stream handle, the stream if it is another than the current one, *outputs) with the context's device
+        current and, so that outputs are allocated for it, the call's stream."""
+        if stream is None and torch.cuda.current_device() == self.dev:
+            return call(_raw_stream(self.dev), None, *outputs)
+        with torch.cuda.device(self.dev):
+            home = torch.cuda.current_stream()
+            if stream is None or stream == home:
+                return call(home.cuda_stream, None, *outputs)
+            if stream.device_index != self.dev:
+                self.fail(f"the stream is not one of the context's device {self.dev}")
+            with torch.cuda.stream(stream):
+                return call(stream.cuda_stream, stream, *outputs)
+
     @staticmethod
-    def plain(dtype):
-        """The float type of a tensor that may hold bf16 bits."""
-        return torch.bfloat16 if dtype in (torch.int16, torch.uint16) else dtype
-
-    @contextlib.contextmanager
-    def on(self, stream):
-        """The context's device and the call's stream, so that outputs are allocated for that stream."""
-        with torch.cuda.device(self.ctx.device):
-            self.home = torch.cuda.current_stream()
-            s = stream if stream is not None else self.home
-            with torch.cuda.stream(s):
-                yield s
-
-    def keep(self, s, *tensors):
+    def keep(s, *tensors):
         """Tell the allocator of tensors used on another stream than the current one, so that memory a caller
         frees right after the call is not given away before the work is done."""
-        if s == self.home or torch.cuda.is_current_stream_capturing():
+        if torch.cuda.is_current_stream_capturing():
             return
         for t in tensors:
             if t is not None:
                 t.record_stream(s)
+
+
+# handle of the current stream of a device, without building a Stream object (5 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _data_ptr(t) -> int:
