@@ -86,7 +86,13 @@ __global__ void __launch_bounds__(kLgThreads) lin_grad_kernel(const LinGradArgs 
     const bool on = c < a.N;   // VEC divides N on the vector path
     const bool want_db = a.db[0] != nullptr || a.db[1] != nullptr;
     int p0, p1;
-    const bool ok = lin_group(a.offsets, a.rows, e, a.err, &p0, &p1);
+    bool ok = true;
+    if (want_db || !a.offsets) {
+        ok = lin_group(a.offsets, a.rows, e, a.err, &p0, &p1);
+    } else {   // the groups do not matter: the rows of all of them
+        p0 = max(0, min(a.rows, __ldg(a.offsets)));
+        p1 = max(p0, min(a.rows, __ldg(a.offsets + a.E)));
+    }
     const int S = gridDim.y, strip = blockIdx.y;
     const int per = (p1 - p0 + S - 1) / S;
     const int r_lo = p0 + min(p1 - p0, strip * per), r_hi = min(p1, r_lo + per);
@@ -96,35 +102,48 @@ __global__ void __launch_bounds__(kLgThreads) lin_grad_kernel(const LinGradArgs 
         s0[i] = 0.0f;
         if (UP) s1[i] = 0.0f;
     }
-    for (int r = r_lo + ty; r < r_hi; r += TY) {
-        const int src = lin_index(a.dy_rows, a.dy_total, r, a.err);
-        if (!on) continue;
-        float dy[VEC], z[VEC], u[VEC], g[VEC];
+    constexpr int U = VEC == 1 ? 4 : 2;   // rows whose loads are in flight together
+    for (int r0 = r_lo + ty; r0 < r_hi; r0 += U * TY) {
+        float dy[U][VEC], z[U][VEC], u[UP ? U : 1][VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) dy[i] = 0.0f;
-        if (src >= 0) lg_load<VEC>(a.dy, static_cast<size_t>(src) * a.lddy + c, a.dy_type, dy);
-        const size_t zi = static_cast<size_t>(r) * a.ldz + c, gi = static_cast<size_t>(r) * a.lddz + c;
-        if (a.act != LACT_NONE) lg_load<VEC>(a.z[0], zi, a.type, z);
-        if (UP) {
-            lg_load<VEC>(a.z[1], zi, a.type, u);
-            float gu[VEC];
+        for (int k = 0; k < U; ++k) {
+            const int r = r0 + k * TY;
+            const int src = r < r_hi ? lin_index(a.dy_rows, a.dy_total, r, a.err) : -1;
+            const size_t zi = static_cast<size_t>(r) * a.ldz + c;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float sg = 1.0f / (1.0f + expf(-z[i]));
-                gu[i] = dy[i] * (z[i] * sg);
-                g[i] = dy[i] * u[i] * (sg * (1.0f + z[i] * (1.0f - sg)));
-                s0[i] += g[i];
-                s1[i] += gu[i];
-            }
-            if (a.dz[1]) lg_store<VEC>(a.dz[1], gi, a.type, gu);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                g[i] = a.act == LACT_NONE ? dy[i] : dy[i] * lin_slope(a.act, z[i]);
-                s0[i] += g[i];
+            for (int i = 0; i < VEC; ++i) dy[k][i] = z[k][i] = 0.0f;
+            if (on && src >= 0) lg_load<VEC>(a.dy, static_cast<size_t>(src) * a.lddy + c, a.dy_type, dy[k]);
+            if (on && r < r_hi && a.act != LACT_NONE) lg_load<VEC>(a.z[0], zi, a.type, z[k]);
+            if (UP) {
+                if (on && r < r_hi) lg_load<VEC>(a.z[1], zi, a.type, u[UP ? k : 0]);
             }
         }
-        if (a.dz[0]) lg_store<VEC>(a.dz[0], gi, a.type, g);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int r = r0 + k * TY;
+            if (!on || r >= r_hi) continue;
+            const size_t gi = static_cast<size_t>(r) * a.lddz + c;
+            float g[VEC];
+            if (UP) {
+                float gu[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float sg = 1.0f / (1.0f + expf(-z[k][i]));
+                    gu[i] = dy[k][i] * (z[k][i] * sg);
+                    g[i] = dy[k][i] * u[UP ? k : 0][i] * (sg * (1.0f + z[k][i] * (1.0f - sg)));
+                    s0[i] += g[i];
+                    s1[UP ? i : 0] += gu[i];
+                }
+                if (a.dz[1]) lg_store<VEC>(a.dz[1], gi, a.type, gu);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    g[i] = a.act == LACT_NONE ? dy[k][i] : dy[k][i] * lin_slope(a.act, z[k][i]);
+                    s0[i] += g[i];
+                }
+            }
+            if (a.dz[0]) lg_store<VEC>(a.dz[0], gi, a.type, g);
+        }
     }
     if (!want_db) return;
 #pragma unroll

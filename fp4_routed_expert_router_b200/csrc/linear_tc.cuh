@@ -36,7 +36,7 @@
 // last row in both operands (a foreign row times zero could still be NaN).
 //
 // Persistent CTAs, one per SM.  Warps: 0 TMA loads, 1 issues the MMAs, 2-3 copy
-// gathered rows (x_rows, by tile::gather4) and ragged ends, 4-11
+// gathered rows (x_rows) and ragged ends, 4-11
 // epilogue (TMEM lane group warp % 4, 16-column units shared by two warps), 12-15
 // (only for operands TMA cannot take: a base that is not 16-byte aligned or
 // rows that are not multiples of 8 values) load element by element.  Two
@@ -62,8 +62,7 @@ constexpr int kLtEpiWarps = 8;
 constexpr int kLtMaxStages = 12;
 constexpr int kLtPromote = 10;       // fp32 outputs: stages summed in the tensor core before the sum moves to registers
 constexpr int kLtRaster = 8;         // row tiles walked together, so that operands of neighbouring tiles meet in L2
-constexpr int kLtOffIdx = 256;       // shared memory: barriers, source rows of the gather (256), tile prefix
-constexpr int kLtOffPrefix = kLtOffIdx + 256 * 4;
+constexpr int kLtOffPrefix = 256;     // shared memory: barriers, then tile prefix, first rows and counts of the groups
 __host__ __device__ constexpr int lt_threads(bool tma) { return (4 + kLtEpiWarps + (tma ? 0 : 4)) * 32; }
 
 struct LtPlan {
@@ -207,26 +206,9 @@ __device__ __forceinline__ void lt_cp16(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
-// Four rows (any rows) x 64 values; the map's box is one row high.
-template <int CG>
-__device__ __forceinline__ void lt_gather4(uint32_t dst, const CUtensorMap* map, int c0, int4 r, uint32_t bar) {
-    if constexpr (CG == 1)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 "
-            "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
-            : "memory");
-}
-
-// Arrive at a barrier anywhere in the cluster and announce `bytes` of copies that complete on it.
-__device__ __forceinline__ void lt_arrive_expect_remote(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+// Several arrivals at a barrier of this CTA.
+__device__ __forceinline__ void lt_arrive_n(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
 // One lane of a converged warp.  The compiler then knows that a single thread issues TMA and MMA instructions; behind
@@ -246,6 +228,11 @@ struct LtRing {
             st = 0;
             ph ^= 1;
         }
+    }
+    __device__ __forceinline__ void skip(int n, int S) {
+        st += n;
+        ph ^= st / S & 1;
+        st %= S;
     }
 };
 
@@ -306,8 +293,9 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* red_full = acc_empty + 2;                    // every part of a split tile is in shared memory
     uint64_t* red_empty = red_full + 1;                    // and has been read
-    int* src_row = reinterpret_cast<int*>(smem + kLtOffIdx);
     int* tprefix = reinterpret_cast<int*>(smem + kLtOffPrefix);   // [E+1] tiles before group e (forward, dgrad)
+    int* gstart = tprefix + a.E + 1;                              // [E] first row of group e
+    int* gcount = gstart + a.E;                                   // [E] its rows, -1: not a sound group
     // split: the parts of this CTA's items (four rows x 32 lanes), [round * warps + warp][rank][4][32]
     float* red = reinterpret_cast<float*>(smem + p.off_red);
     __shared__ uint32_t tmem_base_s;
@@ -342,12 +330,13 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
         }
     }
     pdl_wait();
-    if (!WG && warp == 0) {   // tiles before each group
+    if (warp == 0) {   // the groups, and the tiles before each
         int work = 0;
         for (int base = 0; base < a.E; base += 32) {
             const int e = base + lane;
             int p0 = 0, p1 = 0;
-            if (e < a.E) lin_group(a.offsets, a.rows, e, a.err, &p0, &p1);
+            bool ok = true;
+            if (e < a.E) ok = lin_group(a.offsets, a.rows, e, a.err, &p0, &p1);
             const int mine = (p1 - p0 + BN - 1) / BN * p.n_ct;
             int incl = mine;
 #pragma unroll
@@ -355,7 +344,11 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
                 if (lane >= o) incl += v;
             }
-            if (e < a.E) tprefix[e] = work + incl - mine;
+            if (e < a.E) {
+                tprefix[e] = work + incl - mine;
+                gstart[e] = p0;
+                gcount[e] = ok ? p1 - p0 : -1;
+            }
             work += __shfl_sync(0xFFFFFFFFu, incl, 31);
         }
         if (lane == 0) tprefix[a.E] = work;
@@ -382,9 +375,9 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             t.e = ve % a.E;
             t.which = ve / a.E;
             n_rt = n_rt_w;
-            int p1;
-            if (!lin_group(a.offsets, a.rows, t.e, a.err, &t.p0, &p1)) return false;
-            t.nq = p1 - t.p0;
+            t.p0 = gstart[t.e];
+            t.nq = gcount[t.e];
+            if (t.nq < 0) return false;
             nkb = (t.nq + kLtBK - 1) / kLtBK;
         } else {
             int lo = 0, hi = a.E - 1;   // the last group that starts at or before w (empty groups start where they end)
@@ -408,13 +401,8 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             t.r0 = rt * BN;
             t.nrows = min(BN, a.out_n - t.r0);
         } else {
-            int p0 = 0, p1 = a.rows;
-            if (a.offsets) {
-                p0 = __ldg(a.offsets + t.e);
-                p1 = __ldg(a.offsets + t.e + 1);
-            }
-            t.r0 = p0 + rt * BN;
-            t.nrows = min(BN, p1 - t.r0);
+            t.r0 = gstart[t.e] + rt * BN;
+            t.nrows = min(BN, gcount[t.e] - rt * BN);
         }
         const int step = 16 * cg;
         t.n = (t.nrows + step - 1) / step * step;
@@ -463,8 +451,10 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     const uint32_t sa = ring0 + ring.st * p.stage_bytes, sb = sa + kLtATile;
                     const uint32_t bar = bar0 + ring.st * 8;
                     const bool ragged = WG && copies && t.nq - kb * kLtBK < kLtBK;   // warps 2-3 copy all of it
-                    if (cg == 1 || rank == 0)                                        // both CTAs' bytes
+                    if (cg == 1 || rank == 0) {                                      // both CTAs' bytes
+                        if (copies && !gathers && !ragged) lt_arrive_n(&full[ring.st], 2 * cg);   // in their place
                         mbar_arrive_expect_tx(&full[ring.st], ragged ? 0u : all);
+                    }
                     if (KIND == LIN_FWD) {
                         if (DUAL) {
 #pragma unroll
@@ -508,18 +498,17 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
         }
     } else if (copies && (warp == 2 || warp == 3)) {
         // ------------------------------------------------------------ gathered rows and ragged ends (64 threads)
-        // Gathered rows (forward: the tile's B rows; wgrad: the stage's 64 A rows) come by tile::gather4, four rows x 64
-        // values each, half of them issued by each warp.  Stages that need zeros -- an index that is no row of x, a
-        // group's last stage in wgrad (there both operands) -- are copied in 16-byte pieces and handed over one stage
-        // later, when they have landed.
-        const int lt = tid - 64, wi = warp - 2;
+        // Gathered rows (forward: the tile's B rows; wgrad: the stage's 64 A rows) and, in wgrad, both operands of a
+        // group's last stage, in 16-byte pieces; what has no source (an index that is no row of x, rows behind the
+        // group) becomes zeros.  Each warp copies its rows by itself and hands a stage over when its copies have landed,
+        // `lag` stages later.  (tile::gather4 moves a row in ten cycles, the pieces of a row cost four.)
+        const int wi = warp - 2;
         const uint16_t* xb = static_cast<const uint16_t*>(WG ? a.a[0] : a.b[0]);
-        const long long ldx = WG ? a.lda : a.ldb;
-        const CUtensorMap* xmap = WG ? &maps.a0 : &maps.b0;
+        const int xstep = static_cast<int>((WG ? a.lda : a.ldb) * 2);
         const uint32_t bar0 = cg == 2 ? lt_map(full, 0) : smem_u32(full);
-        LtRing ring;
-        int turn = 0;
-        int pending = -1;            // slot of a copied stage that has not been handed over
+        const int lag = S >= 10 ? 8 : S >= 6 ? 4 : S >= 4 ? 2 : 1;   // (a stage waits ~1 us for its pieces)
+        LtRing ring, out;
+        int flying = 0;              // stages copied and not handed over
         bool stop = false;
         auto source = [&](int r) {   // row of x behind grouped row r, -1: counts as zero
             if (!a.gather) return r;
@@ -528,132 +517,130 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             latch_error(a.err, ERR_EINVAL, r, KID_LINEAR);
             return -1;
         };
-        auto both = [&](bool ok) {   // meet the other warp; whether all threads of both are fine
-            uint32_t r;
-            __syncwarp();
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-                "barrier.cta.red.and.aligned.pred q, 1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                : "=r"(r)
-                : "r"(ok ? 1u : 0u)
-                : "memory");
-            return r != 0;
-        };
-        auto hand_over = [&]() {
-            if (pending < 0) return;
+        auto give = [&]() {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) lt_arrive_remote(bar0 + pending * 8);
-            pending = -1;
+            if (lane == 0) lt_arrive_remote(bar0 + out.st * 8);
+            out.next(S);
+            --flying;
         };
-        auto copy = [&](uint32_t tile, int row, int ch, const uint16_t* base, long long ld, int r, int col, int width) {
-            const int n = r < 0 ? 0 : max(0, min(16, (width - col) * 2));
-            lt_cp16(tile + row * 128 + ((ch ^ (row & 7)) << 4),
-                    n == 0 ? base : base + static_cast<size_t>(r) * ld + col, n);
+        auto copied = [&]() {        // the copies of one more stage are on their way
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (++flying <= lag) return;
+            if (lag == 8) asm volatile("cp.async.wait_group 8;" ::: "memory");
+            else if (lag == 4) asm volatile("cp.async.wait_group 4;" ::: "memory");
+            else if (lag == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+            else asm volatile("cp.async.wait_group 1;" ::: "memory");
+            give();
         };
+        auto slot_free = [&](int kb) -> bool {   // (warp-uniform)
+            int ok = 1;
+            if (lane == 0) {
+                ok = lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, a.timeout_ns);
+                if (!ok) latch_error(a.err, ERR_ETIMEOUT, kb, KID_LINEAR);
+            }
+            return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+        };
+        // bytes of a row of `width` values that the piece from column `col` on holds
+        auto piece = [](int col, int width) { return max(0, min(16, (width - col) * 2)); };
         for (int w = w0; w < n_work && !stop; w += G) {
             LtTile t;
             if (!tile_of(w, t)) continue;
-            bool sound = true;                   // every index is a row of x
-            const int need = max(0, min(t.nb, t.nrows - t.b0));   // forward: rows of this CTA that count
             if (!WG) {
-                both(true);                      // the other warp is done with the last tile's table
-                for (int i = lt; i < t.nb; i += 64) {
-                    const int v = i < need ? source(t.r0 + t.b0 + i) : -1;
-                    sound &= v >= 0 || i >= need;
-                    src_row[i] = v;
+                // lane: piece lane & 7 of rows 4 wi + (lane >> 3) + 8 j; the rows' sources lie in registers, j = (l >> 2)
+                // + 8 k of residue l & 3 in register k of lane l
+                const int need = max(0, min(t.nb, t.nrows - t.b0));   // rows of this CTA that count
+                constexpr int NK = cg == 2 ? 2 : 4;
+                int src[NK];
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    const int i = 4 * wi + (lane & 3) + 8 * ((lane >> 2) + 8 * k);
+                    src[k] = i < need ? source(t.r0 + t.b0 + i) : -1;
                 }
-                sound = both(sound);
+                const int ch = lane & 7, sub = lane >> 3;
+                const uint32_t dst = kLtATile + (4 * wi + sub) * 128 + ((ch ^ (4 * wi + sub)) << 4);
+                for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next(S)) {
+                    if (!slot_free(kb)) {
+                        stop = true;
+                        break;
+                    }
+                    const uint32_t at = ring0 + ring.st * p.stage_bytes + dst;
+                    const int n = piece(kb * kLtBK + ch * 8, a.Q);
+                    const char* from = reinterpret_cast<const char*>(xb + (n ? kb * kLtBK + ch * 8 : 0));
+#pragma unroll
+                    for (int k = 0; k < NK; ++k) {
+                        if (64 * k < t.nb) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {   // (rows up to the next multiple of 64 have a place)
+                                const int r = __shfl_sync(0xFFFFFFFFu, src[k], sub | j << 2);
+                                if (64 * k + 8 * j < t.nb)
+                                    lt_cp16(at + (64 * k + 8 * j) * 128,
+                                            from + static_cast<long long>(max(r, 0)) * xstep, r < 0 ? 0 : n);
+                            }
+                        }
+                    }
+                    copied();
+                }
+                continue;
             }
-            int ahead = WG && gathers && lt < t.nq - t.kb0 * kLtBK && t.kb0 < t.kb1
-                            ? source(t.p0 + t.kb0 * kLtBK + lt) : WG && !gathers ? t.p0 + t.kb0 * kLtBK + lt : -1;
+            // wgrad; lane: piece lane & 15 of rows 2 wi + (lane >> 4) + 4 j, whose source lane (lane >> 4) + 2 j has
+            if (t.kb0 >= t.kb1) continue;
+            if (!gathers) {
+                const int whole = min(t.kb1, t.nq / kLtBK) - t.kb0;   // stages that TMA loads
+                ring.skip(whole, S);
+                t.kb0 += whole;
+            }
+            const int ch = lane & 15, sub = lane >> 4;
+            const int mine = 2 * wi + (lane & 1) + 4 * (lane >> 1);   // the row whose source this lane knows
+            const int na = piece(t.c0 + ch * 8, a.C);
+            const char* from = reinterpret_cast<const char*>(xb + (na ? t.c0 + ch * 8 : 0));
+            const int row0 = 2 * wi + sub;
+            int ahead = t.kb0 < t.kb1 && t.kb0 * kLtBK + mine < t.nq ? source(t.p0 + t.kb0 * kLtBK + mine) : -1;
             for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next(S)) {
                 const int valid = t.nq - kb * kLtBK;
-                const bool ragged = WG && valid < kLtBK;
-                int* table = src_row;
-                if (WG) {
-                    table += turn * 64;
-                    turn ^= 1;
-                }
-                if (WG) {   // two tables in turn: the other one may still be read
-                    sound = ahead >= 0;
-                    table[lt] = lt < valid ? ahead : -1;
-                    const int q = (kb + 1) * kLtBK + lt;
-                    if (gathers) ahead = kb + 1 < t.kb1 && q < t.nq ? source(t.p0 + q) : -1;
-                    else ahead = t.p0 + q;
-                }
-                bool ok = true;
-                if (lane == 0) {
-                    ok = lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, a.timeout_ns);
-                    if (!ok) latch_error(a.err, ERR_ETIMEOUT, kb, KID_LINEAR);
-                }
-                if (!both(ok)) {
+                const int src = ahead;
+                ahead = kb + 1 < t.kb1 && (kb + 1) * kLtBK + mine < t.nq ? source(t.p0 + (kb + 1) * kLtBK + mine) : -1;
+                if (!slot_free(kb)) {
                     stop = true;
                     break;
                 }
-                if (WG) sound = both(sound || ragged);
-                const uint32_t sa = ring0 + ring.st * p.stage_bytes, sb = sa + kLtATile, bar = bar0 + ring.st * 8;
-                if (!ragged && (!gathers || sound)) {
+                const uint32_t sa = ring0 + ring.st * p.stage_bytes;
+                const int rows = min(kLtBK, (valid + 15) / 16 * 16);
+                const uint32_t at = sa + (ch >> 3) * 8192 + row0 * 128;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int r = __shfl_sync(0xFFFFFFFFu, src, sub + 2 * j);
+                    if (4 * j < rows)
+                        lt_cp16(at + 4 * j * 128 + (((ch & 7) ^ ((row0 + 4 * j) & 7)) << 4),
+                                from + static_cast<long long>(max(r, 0)) * xstep, r < 0 ? 0 : na);
+                }
+                if (valid < kLtBK) {   // the group's last stage: B too
+                    const uint16_t* bb = static_cast<const uint16_t*>(a.b[t.which]);
+                    for (int c = ch; c < (t.nb + 63) / 64 * 8; c += 16) {   // 128 values of each row a time
+                        const int col = t.r0 + t.b0 + c * 8, nb = piece(col, a.out_n);
+                        const uint16_t* bp =
+                            bb + static_cast<size_t>(t.p0 + kb * kLtBK + row0) * a.ldb + (nb ? col : 0);
+                        const uint32_t sb = sa + kLtATile + (c >> 3) * 8192 + row0 * 128;
+#pragma unroll 4
+                        for (int j = 0; 4 * j < rows; ++j) {
+                            const bool in = row0 + 4 * j < valid;
+                            lt_cp16(sb + 4 * j * 128 + (((c & 7) ^ ((row0 + 4 * j) & 7)) << 4),
+                                    in ? bp + 4 * j * a.ldb : bb, in ? nb : 0);
+                        }
+                    }
+                }
+                if (gathers) {
+                    copied();
+                } else {   // the next stage copied here may be a ring away
                     asm volatile("cp.async.wait_all;" ::: "memory");
-                    hand_over();
-                    if (lt_elect()) {
-                        if (!gathers) {
-                            lt_arrive_remote(bar);
-                        } else if (!WG) {
-                            const int quads = (need + 3) / 4, mine = (quads + 1 - wi) / 2;
-                            lt_arrive_expect_remote(bar, static_cast<uint32_t>(mine * 512));
-                            for (int q = wi; q < quads; q += 2) {
-                                int4 r = *reinterpret_cast<const int4*>(table + 4 * q);   // behind the last: row 0
-                                r.y = max(r.y, 0);
-                                r.z = max(r.z, 0);
-                                r.w = max(r.w, 0);
-                                lt_gather4<CG>(sb + q * 512, xmap, kb * kLtBK, r, bar);
-                            }
-                        } else {
-                            const int c = t.c0 + 64 * wi;
-                            lt_arrive_expect_remote(bar, c < a.C ? 8192u : 0u);
-                            if (c < a.C) {
-#pragma unroll 4
-                                for (int q = 0; q < 16; ++q)
-                                    lt_gather4<CG>(sa + wi * 8192 + q * 512, xmap, c,
-                                                   *reinterpret_cast<const int4*>(table + 4 * q), bar);
-                            }
-                        }
-                    }
-                    __syncwarp();
-                    continue;
+                    out = ring;
+                    give();
+                    flying = 0;
                 }
-                if (!WG) {
-#pragma unroll 4
-                    for (int i = lt >> 3; i < t.nb; i += 8)
-                        copy(sb, i, lt & 7, xb, ldx, table[i], kb * kLtBK + (lt & 7) * 8, a.Q);
-                } else {
-                    const int rows = ragged ? (valid + 15) / 16 * 16 : kLtBK;
-                    const int ch = lt & 15;
-#pragma unroll 4
-                    for (int i = lt >> 4; i < rows; i += 4)
-                        copy(sa + (ch >> 3) * 8192, i, ch & 7, xb, ldx, table[i], t.c0 + ch * 8, a.C);
-                    if (ragged) {
-                        const uint16_t* bb = static_cast<const uint16_t*>(a.b[t.which]);
-                        const int per = (t.nb + 63) / 64 * 8;   // chunks of a row: 8, 16 or 32 (24: taken as 32)
-                        const int shift = per <= 8 ? 3 : per <= 16 ? 4 : 5;
-#pragma unroll 4
-                        for (int i = lt; i < rows << shift; i += 64) {
-                            const int row = i >> shift, c = i & ((1 << shift) - 1);
-                            if (c < per)
-                                copy(sb + (c >> 3) * 8192, row, c & 7, bb, a.ldb,
-                                     row < valid ? t.p0 + kb * kLtBK + row : -1, t.r0 + t.b0 + c * 8, a.out_n);
-                        }
-                    }
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-                hand_over();
-                pending = ring.st;
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        hand_over();
+        while (flying > 0) give();
     } else if (!TMA && warp >= 4 + kLtEpiWarps) {
         // ------------------------------------------------------------ element loader (128 threads)
         const int lt = tid - (4 + kLtEpiWarps) * 32;
@@ -1110,9 +1097,10 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
 }
 
 // ------------------------------------------------------------------ host side
-// 16-bit tensor map with a 128-byte swizzle, innermost dimension contiguous; strides in elements.
-inline bool lt_encode_n(CUtensorMap* map, int type, const void* base, int rank, const cuuint64_t* dims,
-                        const cuuint64_t* strides, uint32_t rows) {
+// Tensor map of boxes of 64 x `rows` 16-bit values of a stack of matrices, 128-byte swizzle, innermost dimension
+// contiguous; strides in elements.
+inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+                      uint64_t s2, uint32_t rows) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     if (!encode) {
         cudaDriverEntryPointQueryResult q;
@@ -1122,32 +1110,20 @@ inline bool lt_encode_n(CUtensorMap* map, int type, const void* base, int rank, 
             return false;
         encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     }
-    const cuuint64_t bytes[2] = {strides[0] * 2, rank > 2 ? strides[1] * 2 : 0};
+    const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1 * 2, s2 * 2};
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(kLtBK), rows, 1}, es[3] = {1, 1, 1};
-    return encode(map, type == LIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                  static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, bytes, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return encode(map, type == LIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Boxes of 64 x `rows` of a stack of matrices.
-inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
-                      uint64_t s2, uint32_t rows) {
-    const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1, s2};
-    return lt_encode_n(map, type, base, 3, dims, strides, rows);
-}
-
-// Single rows of 64 values, for gathers.
-inline bool lt_encode2(CUtensorMap* map, int type, const void* base, uint64_t d0, uint64_t d1, uint64_t s1) {
-    const cuuint64_t dims[2] = {d0, d1}, strides[1] = {s1};
-    return lt_encode_n(map, type, base, 2, dims, strides, 1);
 }
 
 // Whether TMA can read the operands as they lie: 16-byte aligned bases, strides of whole 16 bytes.
 inline bool lt_tma_ok(const LinArgs& a) {
     auto base = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
     const bool groups = a.kind != LIN_WGRAD && a.E > 1;
-    return base(a.a[0]) && base(a.a[1]) && base(a.b[0]) && base(a.b[1]) && a.lda % 8 == 0 && a.ldb % 8 == 0 &&
+    const long long far = 1LL << 30;   // rows up to 2 GB apart: 32-bit steps in the gather, strides a map can hold
+    return a.lda < far && a.ldb < far && base(a.a[0]) && base(a.a[1]) && base(a.b[0]) && base(a.b[1]) && a.lda % 8 == 0 && a.ldb % 8 == 0 &&
            (!groups || a.a_gstride % 8 == 0);
 }
 
@@ -1164,7 +1140,7 @@ inline double lt_shape(const LinArgs& a, bool tma, int cg, int split, int bn, co
     const int brows = bn / cg;
     p->bbox = brows < 64 ? brows : 64;
     p->stage_bytes = kLtATile + ((wg ? (brows + 63) / 64 * 64 : brows) * 128 + 1023) / 1024 * 1024;
-    p->off_ring = (kLtOffPrefix + 4 * (a.E + 1) + 1023) / 1024 * 1024;
+    p->off_ring = (kLtOffPrefix + 4 * (3 * a.E + 1) + 1023) / 1024 * 1024;
     // items: bn / 4 quarters x 4 lane groups, in rounds of all the cluster's warps
     const int red = split > 1 ? (bn + kLtEpiWarps * split - 1) / (kLtEpiWarps * split) * kLtEpiWarps * split * 512 : 0;
     p->stages = (smem_limit - 1024 - p->off_ring - red) / p->stage_bytes;
@@ -1238,7 +1214,7 @@ inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     bool ok = true;
     if (a.kind == LIN_WGRAD) {   // A = x [rows, C], B = dz [rows, out_n]
         const uint64_t xr = g ? a.gather_total : R;
-        ok = (g ? lt_encode2(&m->a0, a.type, a.a[0], C, xr, lda) : lt_encode(&m->a0, a.type, a.a[0], C, xr, 1, lda, lda * xr, 64)) &&
+        ok = lt_encode(&m->a0, a.type, a.a[0], C, xr, 1, lda, lda * xr, 64) &&
              lt_encode(&m->b0, a.type, a.b[0], a.out_n, R, 1, ldb, ldb * R, 64);
         m->a1 = m->a0;
         m->b1 = m->b0;
@@ -1250,8 +1226,7 @@ inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     const uint64_t br = g && fwd ? a.gather_total : R;
     const uint32_t abox = !fwd ? 64 : a.a[1] ? 16 : kLtM;
     ok = lt_encode(&m->a0, a.type, a.a[0], inner, outer, E, lda, gs, abox) &&
-         (g && fwd ? lt_encode2(&m->b0, a.type, a.b[0], Q, br, ldb)
-                   : lt_encode(&m->b0, a.type, a.b[0], Q, br, 1, ldb, ldb * br, p.bbox));
+         lt_encode(&m->b0, a.type, a.b[0], Q, br, 1, ldb, ldb * br, p.bbox);
     m->a1 = m->a0;
     m->b1 = m->b0;
     if (a.a[1]) ok = ok && lt_encode(&m->a1, a.type, a.a[1], inner, outer, E, lda, gs, abox);

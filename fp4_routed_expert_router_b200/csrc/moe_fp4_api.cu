@@ -949,10 +949,11 @@ cudaError_t lin_run(moe_fp4_ctx* c, const char* name, const LinArgs& a, cudaStre
 
 cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
     const bool db = g.db[0] || g.db[1];
-    // rows a strip should hold: enough for the column sums' epilogue to be small beside the loads
-    const int per_group = g.E > 0 ? (g.rows + g.E - 1) / g.E : g.rows;
-    int strips = per_group / 256;
-    const int most = db ? 8 : 64;              // a portable cluster holds 8 CTAs
+    // Strips of rows.  With db those of a group form a cluster (8 CTAs at most) and should hold enough rows for the
+    // meeting of their sums to be small beside the loads; without it 64 rows a strip keep every SM loading.
+    const int per_group = (g.rows + g.E - 1) / g.E;
+    int strips = db ? per_group / 256 : (g.rows + 63) / 64;
+    const int most = db ? 8 : 65535;
     strips = strips < 1 ? 1 : strips > most ? most : strips;
     auto vec_ok = [](const void* p, long long ld, int type) {
         const uintptr_t step = type == LIN_F32 ? 4 : 8;
@@ -962,7 +963,7 @@ cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
                vec_ok(g.dz[1], g.lddz, g.type) && vec_ok(g.z[0], g.ldz, g.type) && vec_ok(g.z[1], g.ldz, g.type);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((g.N + kLgCols - 1) / kLgCols), static_cast<unsigned>(strips),
-                       static_cast<unsigned>(g.E));
+                       static_cast<unsigned>(db ? g.E : 1));
     cfg.blockDim = dim3(kLgThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
