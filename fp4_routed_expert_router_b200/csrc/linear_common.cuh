@@ -36,8 +36,8 @@ struct LinArgs {
     // B: x, dz and dz_up, or for wgrad dz and dz_up (two outputs)
     const void* b[2];
     long long ldb;
-    const int32_t* gather;    // rows of x: of B (forward) or of A (wgrad), or NULL
-    int gather_total;
+    int b_rows;               // rows that B has (wgrad: that A and B have)
+    int packed;               // those rows lie at lin_packed(first row, group) instead of at the group's rows
     // output
     void* out[2];
     long long ldo, o_gstride;
@@ -123,6 +123,12 @@ __device__ __forceinline__ int lin_index(const int32_t* idx, int total, int r, i
     latch_error(err, ERR_EINVAL, r, KID_LINEAR);
     return -1;
 }
+
+// First row of group e, whose rows start at `start`, in a packed copy: a multiple of 16 with room for the group's rows
+// rounded up to 16 before the next one's (the rounded starts of two groups n rows apart differ by at least n - 15, and
+// 16 are added for each group).  A copy of R rows in E groups takes lin_packed_rows.
+__host__ __device__ __forceinline__ int lin_packed(int start, int e) { return (start + 15) / 16 * 16 + 16 * e; }
+inline long long lin_packed_rows(long long R, long long E) { return (R + 16 * E + 31) / 16 * 16; }
 
 template <int ACT, int N>
 __device__ __forceinline__ void lin_act_all(float (&v)[N], const float (&u)[N]) {

@@ -3,8 +3,8 @@
 
 namespace moe {
 
-cudaError_t lin_launch_dgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
-    return lt_launch<LIN_DGRAD, false>(a, p, m, tma, s);
+cudaError_t lin_launch_dgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s) {
+    return lt_launch<LIN_DGRAD, false>(a, p, m, s);
 }
 
 cudaError_t lin_allow_dgrad(int bytes) { return lt_allow<LIN_DGRAD, false>(bytes); }

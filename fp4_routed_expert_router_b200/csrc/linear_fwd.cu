@@ -3,8 +3,8 @@
 
 namespace moe {
 
-cudaError_t lin_launch_fwd(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
-    return lt_launch<LIN_FWD, false>(a, p, m, tma, s);
+cudaError_t lin_launch_fwd(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s) {
+    return lt_launch<LIN_FWD, false>(a, p, m, s);
 }
 
 cudaError_t lin_allow_fwd(int bytes) { return lt_allow<LIN_FWD, false>(bytes); }
@@ -13,7 +13,7 @@ cudaError_t lin_slots(int smem, int* slots) {
     for (int n = 1; n <= 8; ++n) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(n));
-        cfg.blockDim = dim3(static_cast<unsigned>(lt_threads(true)));
+        cfg.blockDim = dim3(static_cast<unsigned>(kLtThreads));
         cfg.dynamicSmemBytes = static_cast<size_t>(smem);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -22,7 +22,7 @@ cudaError_t lin_slots(int smem, int* slots) {
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&slots[n], lin_tc_kernel<LIN_FWD, false, true, 1, false>, &cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&slots[n], lin_tc_kernel<LIN_FWD, false, 1, false>, &cfg);
         if (e != cudaSuccess) return e;
         if (slots[n] < 1) return cudaErrorInvalidConfiguration;
     }

@@ -27,6 +27,7 @@ struct LinGradArgs {
     long long ldz;
     void* dz[2];              // may be NULL (only db is wanted)
     long long lddz;
+    int packed;               // rows of dz at lin_packed, zeros behind each group up to the next multiple of 16
     float* db[2];
     int accumulate;
     int* err;
@@ -72,7 +73,8 @@ __device__ __forceinline__ void lg_store(void* p, size_t at, int type, const flo
     }
 }
 
-// grid (column blocks, row strips, groups); with db the strips of a group form one cluster.
+// grid (column blocks, row strips, groups); with db the strips of a group form one cluster.  Without db and without
+// packing the rows of all groups are strips of one.
 template <int VEC, bool UP>
 __global__ void __launch_bounds__(kLgThreads) lin_grad_kernel(const LinGradArgs a) {
     namespace cg = cooperative_groups;
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kLgThreads) lin_grad_kernel(const LinGradArgs 
     const bool want_db = a.db[0] != nullptr || a.db[1] != nullptr;
     int p0, p1;
     bool ok = true;
-    if (want_db || !a.offsets) {
+    if (want_db || a.packed || !a.offsets) {
         ok = lin_group(a.offsets, a.rows, e, a.err, &p0, &p1);
     } else {   // the groups do not matter: the rows of all of them
         p0 = max(0, min(a.rows, __ldg(a.offsets)));
@@ -96,6 +98,19 @@ __global__ void __launch_bounds__(kLgThreads) lin_grad_kernel(const LinGradArgs 
     const int S = gridDim.y, strip = blockIdx.y;
     const int per = (p1 - p0 + S - 1) / S;
     const int r_lo = p0 + min(p1 - p0, strip * per), r_hi = min(p1, r_lo + per);
+    // first row of the strip's rows in dz, from r = 0 on
+    const long long g0 = a.packed ? static_cast<long long>(lin_packed(p0, e)) - p0 : 0;
+    if (a.packed && ok && strip == 0 && on) {   // zeros behind the group
+        const int end = p1 - p0 + ((p0 - p1) & 15);
+        float zero[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) zero[i] = 0.0f;
+        for (int r = p1 - p0 + ty; r < end; r += TY) {
+            const size_t gi = static_cast<size_t>(g0 + p0 + r) * a.lddz + c;
+            lg_store<VEC>(a.dz[0], gi, a.type, zero);
+            if (UP) lg_store<VEC>(a.dz[1], gi, a.type, zero);
+        }
+    }
     float s0[VEC], s1[UP ? VEC : 1];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
@@ -122,7 +137,7 @@ __global__ void __launch_bounds__(kLgThreads) lin_grad_kernel(const LinGradArgs 
         for (int k = 0; k < U; ++k) {
             const int r = r0 + k * TY;
             if (!on || r >= r_hi) continue;
-            const size_t gi = static_cast<size_t>(r) * a.lddz + c;
+            const size_t gi = static_cast<size_t>(g0 + r) * a.lddz + c;
             float g[VEC];
             if (UP) {
                 float gu[VEC];

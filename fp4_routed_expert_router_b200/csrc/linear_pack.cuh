@@ -1,0 +1,117 @@
+// linear_pack.cuh -- copies of operands that the tensor-core kernels cannot read
+// as they lie: rows of x gathered through an index, the rows of wgrad's groups
+// with zeros behind each group, and matrices whose base or rows are not 16-byte
+// aligned.  Bound by memory: each value is read and written once, 16 bytes a
+// thread at a time (what is not aligned is read in the widest pieces that stay
+// inside it).  A block copies 16 rows x 512 columns; rows of a packed copy come
+// in sixteens that belong to one group (lin_packed).
+#pragma once
+#include "linear_common.cuh"
+
+namespace moe {
+
+constexpr int kLpRows = 16, kLpCols = 512, kLpThreads = 256;
+
+struct LinPackJob {
+    const uint16_t* src;
+    uint16_t* dst;
+    long long lds, ldd;      // row strides; ldd is a multiple of 8 and dst 16-byte aligned
+    long long gstride;       // weights: elements from one group's matrix to the next in src
+    int cols;
+    int rows;                // weights: rows of one group's matrix; 0: the grouped rows of x
+};
+
+struct LinPackArgs {
+    const int32_t* offsets;  // NULL: one group of all rows
+    int E, rows;
+    int packed;              // x: rows at lin_packed (else where they are)
+    const int32_t* index;    // x: source rows, or NULL
+    int total;
+    LinPackJob job[3];
+    int* err;
+};
+
+// Eight 16-bit values from any 2-byte aligned address, zeros from value n on: the widest loads that stay inside them.
+__device__ __forceinline__ uint4 lin_chunk(const uint16_t* s, int n) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (n >= 8) {
+        const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s));
+        if ((at & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(s));
+        if ((at & 3) == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
+        } else {
+            const uint32_t* m = reinterpret_cast<const uint32_t*>(s + 1);
+            const uint32_t a = __ldg(s), b = __ldg(m), c = __ldg(m + 1), d = __ldg(m + 2), e = __ldg(s + 7);
+            w[0] = a | b << 16;
+            w[1] = __funnelshift_l(b, c, 16);
+            w[2] = __funnelshift_l(c, d, 16);
+            w[3] = d >> 16 | e << 16;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < n) w[i >> 1] |= static_cast<uint32_t>(__ldg(s + i)) << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// grid (row blocks of the largest job, column blocks, jobs)
+__global__ void __launch_bounds__(kLpThreads) lin_pack_kernel(const LinPackArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const LinPackJob& j = a.job[blockIdx.z];
+    const int c0 = blockIdx.y * kLpCols;
+    if (c0 >= j.ldd) return;
+    const int pieces = min(kLpCols, static_cast<int>(j.ldd) - c0) / 8;   // of a row
+    const uint16_t* src = j.src;
+    uint16_t* dst = j.dst;
+    int row0, rows, have, p0 = 0;   // rows row0 .. row0 + rows of dst; the first `have` are copied, the others zero
+    if (j.rows) {   // a weight: only of groups that have rows
+        const int per = (j.rows + kLpRows - 1) / kLpRows;
+        const int e = blockIdx.x / per;
+        int q0, q1;
+        if (e >= a.E || !lin_group(a.offsets, a.rows, e, a.err, &q0, &q1) || q0 == q1) return;
+        row0 = (blockIdx.x - e * per) * kLpRows;
+        rows = have = min(kLpRows, j.rows - row0);
+        src += static_cast<size_t>(e) * j.gstride;
+        dst += static_cast<size_t>(e) * j.rows * j.ldd;
+        p0 = row0;
+    } else if (!a.packed) {   // grouped rows as they are; none outside the groups
+        const int lo = a.offsets ? max(0, __ldg(a.offsets)) : 0;
+        const int hi = a.offsets ? min(a.rows, __ldg(a.offsets + a.E)) : a.rows;
+        row0 = p0 = max(lo, static_cast<int>(blockIdx.x) * kLpRows);
+        rows = have = min(hi, static_cast<int>(blockIdx.x + 1) * kLpRows) - row0;
+    } else {   // the group of these sixteen rows: the last that starts at or before them
+        row0 = blockIdx.x * kLpRows;
+        int lo = 0, hi = a.E;
+        while (hi - lo > 1) {   // 32 probes at a time
+            const int step = (hi - lo + 31) / 32, e = lo + (threadIdx.x & 31) * step;
+            const bool before = e < hi && lin_packed(__ldg(a.offsets + e), e) <= row0;
+            const int n = __popc(__ballot_sync(0xFFFFFFFFu, before));
+            const int first = n > 0 ? lo + (n - 1) * step : lo;
+            hi = min(hi, first + step);
+            lo = first;
+        }
+        int q0, q1;
+        if (!lin_group(a.offsets, a.rows, lo, a.err, &q0, &q1)) return;
+        const int in = row0 - lin_packed(q0, lo);
+        if (in < 0 || in >= q1 - q0) return;   // no rows of a group
+        rows = kLpRows;
+        have = min(kLpRows, q1 - q0 - in);
+        p0 = q0 + in;
+    }
+    if (rows <= 0) return;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < rows * pieces; i += kLpThreads) {
+        const int r = i / pieces, c = c0 + (i - r * pieces) * 8;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < have) {
+            const int from = j.rows ? p0 + r : lin_index(a.index, a.total, p0 + r, a.err);
+            if (from >= 0) v = lin_chunk(src + static_cast<size_t>(from) * j.lds + c, j.cols - c);
+        }
+        *reinterpret_cast<uint4*>(dst + static_cast<size_t>(row0 + r) * j.ldd + c) = v;
+    }
+}
+
+}  // namespace moe

@@ -3,8 +3,8 @@
 
 namespace moe {
 
-cudaError_t lin_launch_swiglu(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
-    return lt_launch<LIN_FWD, true>(a, p, m, tma, s);
+cudaError_t lin_launch_swiglu(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s) {
+    return lt_launch<LIN_FWD, true>(a, p, m, s);
 }
 
 cudaError_t lin_allow_swiglu(int bytes) { return lt_allow<LIN_FWD, true>(bytes); }

@@ -32,14 +32,11 @@
 // Groups: rows of a tile belong to one group; a tile that ends inside a group's
 // last rows reads what lies behind them into columns that are not stored.  In
 // wgrad the group is the sum: its last stage runs only the 16-term steps it
-// needs and is copied by the gather warps, which put zeros behind the group's
-// last row in both operands (a foreign row times zero could still be NaN).
+// needs, and both operands come packed with zeros up to the next multiple of 16
+// (linear_pack.cuh), as a foreign row times zero could still be NaN.
 //
-// Persistent CTAs, one per SM.  Warps: 0 TMA loads, 1 issues the MMAs, 2-3 copy
-// gathered rows (x_rows) and ragged ends, 4-11
-// epilogue (TMEM lane group warp % 4, 16-column units shared by two warps), 12-15
-// (only for operands TMA cannot take: a base that is not 16-byte aligned or
-// rows that are not multiples of 8 values) load element by element.  Two
+// Persistent CTAs, one per SM.  Warps: 0 TMA loads, 1 issues the MMAs, 4-11
+// epilogue (TMEM lane group warp % 4, 16-column units shared by two warps).  Two
 // accumulators, so the epilogue of a tile overlaps the next one's products.
 // fp32 outputs: the tensor core cuts its sums (measured 1e-9 relative per term,
 // always towards zero), so spans of 640 terms are added up in registers.
@@ -63,7 +60,7 @@ constexpr int kLtMaxStages = 12;
 constexpr int kLtPromote = 10;       // fp32 outputs: stages summed in the tensor core before the sum moves to registers
 constexpr int kLtRaster = 8;         // row tiles walked together, so that operands of neighbouring tiles meet in L2
 constexpr int kLtOffPrefix = 256;     // shared memory: barriers, then tile prefix, first rows and counts of the groups
-__host__ __device__ constexpr int lt_threads(bool tma) { return (4 + kLtEpiWarps + (tma ? 0 : 4)) * 32; }
+constexpr int kLtThreads = (4 + kLtEpiWarps) * 32;
 
 struct LtPlan {
     int bn;         // output rows of a tile
@@ -201,16 +198,6 @@ __device__ __forceinline__ void lt_tma3(uint32_t dst, const CUtensorMap* map, in
             : "memory");
 }
 
-// 16 bytes, of which the last 16 - n are zeros.
-__device__ __forceinline__ void lt_cp16(uint32_t dst, const void* src, int n) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-
-// Several arrivals at a barrier of this CTA.
-__device__ __forceinline__ void lt_arrive_n(uint64_t* bar, uint32_t n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
-}
-
 // One lane of a converged warp.  The compiler then knows that a single thread issues TMA and MMA instructions; behind
 // a plain lane test it serialises each of them over the warp (75 cycles apiece, measured).
 __device__ __forceinline__ bool lt_elect() {
@@ -229,64 +216,31 @@ struct LtRing {
             ph ^= 1;
         }
     }
-    __device__ __forceinline__ void skip(int n, int S) {
-        st += n;
-        ph ^= st / S & 1;
-        st %= S;
-    }
 };
-
-// Eight 16-bit values from any 2-byte aligned address, zeros from value n on: the widest loads that stay inside them.
-__device__ __forceinline__ uint4 lt_chunk(const uint16_t* s, int n) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (n >= 8) {
-        const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s));
-        if ((at & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(s));
-        if ((at & 3) == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
-        } else {
-            const uint32_t* m = reinterpret_cast<const uint32_t*>(s + 1);
-            const uint32_t a = __ldg(s), b = __ldg(m), c = __ldg(m + 1), d = __ldg(m + 2), e = __ldg(s + 7);
-            w[0] = a | b << 16;
-            w[1] = __funnelshift_l(b, c, 16);
-            w[2] = __funnelshift_l(c, d, 16);
-            w[3] = d >> 16 | e << 16;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-            if (i < n) w[i >> 1] |= static_cast<uint32_t>(__ldg(s + i)) << (16 * (i & 1));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 struct LtTile {
     int e, which;   // group, output (wgrad: dw or dw_up)
     int c0;         // first c of this CTA
     int r0, nrows;  // first output row (forward, dgrad: grouped row; wgrad: row of the group's output), rows
-    int p0, nq;     // wgrad: the group's first row and row count
+    int p0, nq;     // first row in B (wgrad: in A and B); terms of the sum
     int kb0, kb1;   // this CTA's stages of the sum
     int n;          // N of the MMA
     int b0;         // first B row of this CTA, from r0
     int nb;         // B rows of this CTA's stage
 };
 
-template <int KIND, bool DUAL, bool TMA, int CG, bool SPANS>
-__global__ void __launch_bounds__(lt_threads(TMA), 1)
+template <int KIND, bool DUAL, int CG, bool SPANS>
+__global__ void __launch_bounds__(kLtThreads, 1)
 lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps maps) {
     constexpr bool WG = KIND == LIN_WGRAD;
     constexpr bool A_MN = KIND != LIN_FWD;
     extern __shared__ __align__(1024) uint8_t lt_smem_raw[];
     uint8_t* smem = lt_smem_raw + ((1024u - (smem_u32(lt_smem_raw) & 1023u)) & 1023u);
     const int S = p.stages, BN = p.bn;
-    static_assert(TMA || CG == 1);
     constexpr int cg = CG;
     const int split = CG == 1 ? p.split : 1;
     const int csize = cg * split;                          // CTAs of a cluster (one of the two is 1)
     const int rank = csize > 1 ? static_cast<int>(lt_rank()) : 0;
-    const bool gathers = a.gather != nullptr && KIND != LIN_DGRAD && TMA;
-    const bool copies = gathers || (WG && TMA && a.offsets != nullptr);   // warps 2-3 take part in every stage
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + kLtMaxStages;
     uint64_t* acc_full = empty + kLtMaxStages;
@@ -305,7 +259,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], TMA ? 1 + (copies ? 2 * cg : 0) : 4);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int q = 0; q < 2; ++q) {
@@ -375,7 +329,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             t.e = ve % a.E;
             t.which = ve / a.E;
             n_rt = n_rt_w;
-            t.p0 = gstart[t.e];
+            t.p0 = a.packed ? lin_packed(gstart[t.e], t.e) : gstart[t.e];
             t.nq = gcount[t.e];
             if (t.nq < 0) return false;
             nkb = (t.nq + kLtBK - 1) / kLtBK;
@@ -388,7 +342,6 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             t.e = lo;
             v = w - tprefix[lo];
             n_rt = (tprefix[lo + 1] - tprefix[lo]) / p.n_ct;
-            t.p0 = 0;
             t.nq = a.Q;
             nkb = (a.Q + kLtBK - 1) / kLtBK * (KIND == LIN_DGRAD && a.b[1] ? 2 : 1);
         }
@@ -402,6 +355,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             t.nrows = min(BN, a.out_n - t.r0);
         } else {
             t.r0 = gstart[t.e] + rt * BN;
+            t.p0 = a.packed ? lin_packed(gstart[t.e], t.e) + rt * BN : t.r0;
             t.nrows = min(BN, gcount[t.e] - rt * BN);
         }
         const int step = 16 * cg;
@@ -420,12 +374,12 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     auto stage_b = [&](int st) { return stage_a(st) + kLtATile; };
     const int half_kb = (a.Q + kLtBK - 1) / kLtBK;   // dgrad: stages of the first pair
     const uint32_t ring0 = smem_u32(smem + p.off_ring);
-    const bool epilogue = warp >= 4 && warp < 4 + kLtEpiWarps;
+    const bool epilogue = warp >= 4;
     // The epilogue of the span kernels holds a tile's sums in registers: 128 a thread on top of its work.  384 threads
     // start with 168 each; 128 x 56 + 256 x 224 is the same number.
     if (!epilogue) {
-    if constexpr (SPANS && TMA) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (TMA && warp == 0) {
+    if constexpr (SPANS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lt_elect()) {
             LtRing ring;
@@ -434,14 +388,12 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             const uint32_t bar0 = cg == 2 ? lt_map(full, 0) : smem_u32(full);
             // this CTA's B boxes: rows b0 .. b0 + nb, none behind the tile's last row
             const int bstep = WG ? 64 : p.bbox, box_b = bstep * 128;
-            const bool a_tma = !(gathers && WG), b_tma = !(gathers && !WG);
             for (int w = w0; w < n_work && !stop; w += G) {
                 LtTile t;
                 if (!tile_of(w, t)) continue;
                 const int nbox = (t.nb + bstep - 1) / bstep;
-                const uint32_t all =
-                    static_cast<uint32_t>(cg * ((a_tma ? kLtATile : 0) + (b_tma ? nbox * box_b : 0)));
-                const int br = t.r0 + t.b0;
+                const uint32_t all = static_cast<uint32_t>(cg * (kLtATile + nbox * box_b));
+                const int br = (WG ? t.r0 : t.p0) + t.b0;
                 for (int kb = t.kb0; kb < t.kb1; ++kb, ++g, ring.next(S)) {
                     if (!lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, a.timeout_ns)) {
                         latch_error(a.err, ERR_ETIMEOUT, g, KID_LINEAR);
@@ -450,11 +402,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     }
                     const uint32_t sa = ring0 + ring.st * p.stage_bytes, sb = sa + kLtATile;
                     const uint32_t bar = bar0 + ring.st * 8;
-                    const bool ragged = WG && copies && t.nq - kb * kLtBK < kLtBK;   // warps 2-3 copy all of it
-                    if (cg == 1 || rank == 0) {                                      // both CTAs' bytes
-                        if (copies && !gathers && !ragged) lt_arrive_n(&full[ring.st], 2 * cg);   // in their place
-                        mbar_arrive_expect_tx(&full[ring.st], ragged ? 0u : all);
-                    }
+                    if (cg == 1 || rank == 0) mbar_arrive_expect_tx(&full[ring.st], all);   // both CTAs' bytes
                     if (KIND == LIN_FWD) {
                         if (DUAL) {
 #pragma unroll
@@ -465,9 +413,8 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                         } else {
                             lt_tma3<CG>(sa, &maps.a0, kb * kLtBK, t.c0, t.e, bar);
                         }
-                        if (b_tma)
-                            for (int b = 0; b < nbox; ++b)
-                                lt_tma3<CG>(sb + b * box_b, &maps.b0, kb * kLtBK, br + b * bstep, 0, bar);
+                        for (int b = 0; b < nbox; ++b)
+                            lt_tma3<CG>(sb + b * box_b, &maps.b0, kb * kLtBK, br + b * bstep, 0, bar);
                     } else if (KIND == LIN_DGRAD) {
                         const bool second = kb >= half_kb;
                         const int q = (second ? kb - half_kb : kb) * kLtBK;
@@ -476,12 +423,10 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                         lt_tma3<CG>(sa, ma, t.c0, q, t.e, bar);
                         lt_tma3<CG>(sa + 8192, ma, t.c0 + 64, q, t.e, bar);
                         for (int b = 0; b < nbox; ++b) lt_tma3<CG>(sb + b * box_b, mb, q, br + b * bstep, 0, bar);
-                    } else if (!ragged) {
+                    } else {
                         const CUtensorMap* mb = t.which ? &maps.b1 : &maps.b0;
-                        if (a_tma) {
-                            lt_tma3<CG>(sa, &maps.a0, t.c0, t.p0 + kb * kLtBK, 0, bar);
-                            lt_tma3<CG>(sa + 8192, &maps.a0, t.c0 + 64, t.p0 + kb * kLtBK, 0, bar);
-                        }
+                        lt_tma3<CG>(sa, &maps.a0, t.c0, t.p0 + kb * kLtBK, 0, bar);
+                        lt_tma3<CG>(sa + 8192, &maps.a0, t.c0 + 64, t.p0 + kb * kLtBK, 0, bar);
                         for (int b = 0; b < nbox; ++b)
                             lt_tma3<CG>(sb + b * box_b, mb, br + b * bstep, t.p0 + kb * kLtBK, 0, bar);
                     }
@@ -494,228 +439,6 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     fresh = 0;
                     mbar_wait(&full[st], (last / S) & 1, &fresh);
                 }
-            }
-        }
-    } else if (copies && (warp == 2 || warp == 3)) {
-        // ------------------------------------------------------------ gathered rows and ragged ends (64 threads)
-        // Gathered rows (forward: the tile's B rows; wgrad: the stage's 64 A rows) and, in wgrad, both operands of a
-        // group's last stage, in 16-byte pieces; what has no source (an index that is no row of x, rows behind the
-        // group) becomes zeros.  Each warp copies its rows by itself and hands a stage over when its copies have landed,
-        // `lag` stages later.  (tile::gather4 moves a row in ten cycles, the pieces of a row cost four.)
-        const int wi = warp - 2;
-        const uint16_t* xb = static_cast<const uint16_t*>(WG ? a.a[0] : a.b[0]);
-        const int xstep = static_cast<int>((WG ? a.lda : a.ldb) * 2);
-        const uint32_t bar0 = cg == 2 ? lt_map(full, 0) : smem_u32(full);
-        const int lag = S >= 10 ? 8 : S >= 6 ? 4 : S >= 4 ? 2 : 1;   // (a stage waits ~1 us for its pieces)
-        LtRing ring, out;
-        int flying = 0;              // stages copied and not handed over
-        bool stop = false;
-        auto source = [&](int r) {   // row of x behind grouped row r, -1: counts as zero
-            if (!a.gather) return r;
-            const int v = __ldg(a.gather + r);
-            if (v >= 0 && v < a.gather_total) return v;
-            latch_error(a.err, ERR_EINVAL, r, KID_LINEAR);
-            return -1;
-        };
-        auto give = [&]() {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) lt_arrive_remote(bar0 + out.st * 8);
-            out.next(S);
-            --flying;
-        };
-        auto copied = [&]() {        // the copies of one more stage are on their way
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (++flying <= lag) return;
-            if (lag == 8) asm volatile("cp.async.wait_group 8;" ::: "memory");
-            else if (lag == 4) asm volatile("cp.async.wait_group 4;" ::: "memory");
-            else if (lag == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-            else asm volatile("cp.async.wait_group 1;" ::: "memory");
-            give();
-        };
-        auto slot_free = [&](int kb) -> bool {   // (warp-uniform)
-            int ok = 1;
-            if (lane == 0) {
-                ok = lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, a.timeout_ns);
-                if (!ok) latch_error(a.err, ERR_ETIMEOUT, kb, KID_LINEAR);
-            }
-            return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
-        };
-        // bytes of a row of `width` values that the piece from column `col` on holds
-        auto piece = [](int col, int width) { return max(0, min(16, (width - col) * 2)); };
-        for (int w = w0; w < n_work && !stop; w += G) {
-            LtTile t;
-            if (!tile_of(w, t)) continue;
-            if (!WG) {
-                // lane: piece lane & 7 of rows 4 wi + (lane >> 3) + 8 j; the rows' sources lie in registers, j = (l >> 2)
-                // + 8 k of residue l & 3 in register k of lane l
-                const int need = max(0, min(t.nb, t.nrows - t.b0));   // rows of this CTA that count
-                constexpr int NK = cg == 2 ? 2 : 4;
-                int src[NK];
-#pragma unroll
-                for (int k = 0; k < NK; ++k) {
-                    const int i = 4 * wi + (lane & 3) + 8 * ((lane >> 2) + 8 * k);
-                    src[k] = i < need ? source(t.r0 + t.b0 + i) : -1;
-                }
-                const int ch = lane & 7, sub = lane >> 3;
-                const uint32_t dst = kLtATile + (4 * wi + sub) * 128 + ((ch ^ (4 * wi + sub)) << 4);
-                for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next(S)) {
-                    if (!slot_free(kb)) {
-                        stop = true;
-                        break;
-                    }
-                    const uint32_t at = ring0 + ring.st * p.stage_bytes + dst;
-                    const int n = piece(kb * kLtBK + ch * 8, a.Q);
-                    const char* from = reinterpret_cast<const char*>(xb + (n ? kb * kLtBK + ch * 8 : 0));
-#pragma unroll
-                    for (int k = 0; k < NK; ++k) {
-                        if (64 * k < t.nb) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {   // (rows up to the next multiple of 64 have a place)
-                                const int r = __shfl_sync(0xFFFFFFFFu, src[k], sub | j << 2);
-                                if (64 * k + 8 * j < t.nb)
-                                    lt_cp16(at + (64 * k + 8 * j) * 128,
-                                            from + static_cast<long long>(max(r, 0)) * xstep, r < 0 ? 0 : n);
-                            }
-                        }
-                    }
-                    copied();
-                }
-                continue;
-            }
-            // wgrad; lane: piece lane & 15 of rows 2 wi + (lane >> 4) + 4 j, whose source lane (lane >> 4) + 2 j has
-            if (t.kb0 >= t.kb1) continue;
-            if (!gathers) {
-                const int whole = min(t.kb1, t.nq / kLtBK) - t.kb0;   // stages that TMA loads
-                ring.skip(whole, S);
-                t.kb0 += whole;
-            }
-            const int ch = lane & 15, sub = lane >> 4;
-            const int mine = 2 * wi + (lane & 1) + 4 * (lane >> 1);   // the row whose source this lane knows
-            const int na = piece(t.c0 + ch * 8, a.C);
-            const char* from = reinterpret_cast<const char*>(xb + (na ? t.c0 + ch * 8 : 0));
-            const int row0 = 2 * wi + sub;
-            int ahead = t.kb0 < t.kb1 && t.kb0 * kLtBK + mine < t.nq ? source(t.p0 + t.kb0 * kLtBK + mine) : -1;
-            for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next(S)) {
-                const int valid = t.nq - kb * kLtBK;
-                const int src = ahead;
-                ahead = kb + 1 < t.kb1 && (kb + 1) * kLtBK + mine < t.nq ? source(t.p0 + (kb + 1) * kLtBK + mine) : -1;
-                if (!slot_free(kb)) {
-                    stop = true;
-                    break;
-                }
-                const uint32_t sa = ring0 + ring.st * p.stage_bytes;
-                const int rows = min(kLtBK, (valid + 15) / 16 * 16);
-                const uint32_t at = sa + (ch >> 3) * 8192 + row0 * 128;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int r = __shfl_sync(0xFFFFFFFFu, src, sub + 2 * j);
-                    if (4 * j < rows)
-                        lt_cp16(at + 4 * j * 128 + (((ch & 7) ^ ((row0 + 4 * j) & 7)) << 4),
-                                from + static_cast<long long>(max(r, 0)) * xstep, r < 0 ? 0 : na);
-                }
-                if (valid < kLtBK) {   // the group's last stage: B too
-                    const uint16_t* bb = static_cast<const uint16_t*>(a.b[t.which]);
-                    for (int c = ch; c < (t.nb + 63) / 64 * 8; c += 16) {   // 128 values of each row a time
-                        const int col = t.r0 + t.b0 + c * 8, nb = piece(col, a.out_n);
-                        const uint16_t* bp =
-                            bb + static_cast<size_t>(t.p0 + kb * kLtBK + row0) * a.ldb + (nb ? col : 0);
-                        const uint32_t sb = sa + kLtATile + (c >> 3) * 8192 + row0 * 128;
-#pragma unroll 4
-                        for (int j = 0; 4 * j < rows; ++j) {
-                            const bool in = row0 + 4 * j < valid;
-                            lt_cp16(sb + 4 * j * 128 + (((c & 7) ^ ((row0 + 4 * j) & 7)) << 4),
-                                    in ? bp + 4 * j * a.ldb : bb, in ? nb : 0);
-                        }
-                    }
-                }
-                if (gathers) {
-                    copied();
-                } else {   // the next stage copied here may be a ring away
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    out = ring;
-                    give();
-                    flying = 0;
-                }
-            }
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        while (flying > 0) give();
-    } else if (!TMA && warp >= 4 + kLtEpiWarps) {
-        // ------------------------------------------------------------ element loader (128 threads)
-        const int lt = tid - (4 + kLtEpiWarps) * 32;
-        LtRing ring;
-        bool stop = false;
-        for (int w = w0; w < n_work && !stop; w += G) {
-            LtTile t;
-            if (!tile_of(w, t)) continue;
-            for (int kb = t.kb0; kb < t.kb1; ++kb, ring.next(S)) {
-                const int st = ring.st;
-                int ok = 1;
-                if (lane == 0) ok = lt_poll<0>(&empty[st], ring.ph ^ 1, abort_flag, a.timeout_ns);
-                if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
-                    if (lane == 0) latch_error(a.err, ERR_ETIMEOUT, kb, KID_LINEAR);
-                    stop = true;
-                    break;
-                }
-                const bool second = KIND == LIN_DGRAD && kb >= half_kb;
-                const int q0 = (second ? kb - half_kb : kb) * kLtBK;
-                const int nq = min(kLtBK, t.nq - q0);
-                // rows of 64 contiguous values (zeros from n on, or where there is no row), a chunk of eight a thread
-                auto fill = [&](uint8_t* tile, int rows, auto src_of, int n) {
-#pragma unroll 4
-                    for (int i = lt; i < rows * 8; i += 128) {
-                        const int sr = i >> 3, ch = i & 7;
-                        const uint16_t* s = src_of(sr);
-                        *reinterpret_cast<uint4*>(tile + sr * 128 + ((ch ^ (sr & 7)) << 4)) =
-                            lt_chunk(s ? s + ch * 8 : nullptr, s ? n - ch * 8 : 0);
-                    }
-                };
-                uint8_t* sa = stage_a(st);
-                uint8_t* sb = stage_b(st);
-                if (KIND == LIN_FWD) {
-                    const size_t at = static_cast<size_t>(t.e) * a.a_gstride + q0;
-                    const uint16_t* w0p = static_cast<const uint16_t*>(a.a[0]) + at;
-                    const uint16_t* w1p = static_cast<const uint16_t*>(a.a[1]) + at;
-                    fill(sa, kLtM,
-                         [&](int sr) -> const uint16_t* {
-                             const int c = t.c0 + (DUAL ? (sr >> 5) * 16 + (sr & 15) : sr);
-                             const uint16_t* base = DUAL && (sr & 16) ? w1p : w0p;
-                             return c < a.C ? base + static_cast<size_t>(c) * a.lda : nullptr;
-                         }, nq);
-                } else {
-                    const uint16_t* base = static_cast<const uint16_t*>(a.a[second ? 1 : 0]) +
-                                           (WG ? 0 : static_cast<size_t>(t.e) * a.a_gstride);
-                    for (int blk = 0; blk < 2; ++blk) {
-                        const int c = t.c0 + 64 * blk;
-                        fill(sa + blk * 8192, kLtBK,
-                             [&](int sr) -> const uint16_t* {
-                                 if (sr >= nq) return nullptr;
-                                 int row = q0 + sr;
-                                 if (WG) row = lin_index(a.gather, a.gather_total, t.p0 + row, a.err);
-                                 return row < 0 ? nullptr : base + static_cast<size_t>(row) * a.lda + c;
-                             }, a.C - c);
-                    }
-                }
-                const uint16_t* bb = static_cast<const uint16_t*>(a.b[WG ? t.which : second ? 1 : 0]);
-                if (WG) {
-                    for (int blk = 0; blk * 64 < t.nrows; ++blk)
-                        fill(sb + blk * 8192, kLtBK,
-                             [&](int sr) -> const uint16_t* {
-                                 return sr < nq ? bb + static_cast<size_t>(t.p0 + q0 + sr) * a.ldb + t.r0 + 64 * blk
-                                                : nullptr;
-                             }, t.nrows - 64 * blk);
-                } else {
-                    fill(sb, t.nrows,
-                         [&](int sr) -> const uint16_t* {
-                             int row = t.r0 + sr;
-                             if (KIND == LIN_FWD) row = lin_index(a.gather, a.gather_total, row, a.err);
-                             return row < 0 ? nullptr : bb + static_cast<size_t>(row) * a.ldb + q0;
-                         }, nq);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[st]);
             }
         }
     } else if (warp == 1 && (cg == 1 || rank == 0)) {
@@ -763,7 +486,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     }
     } else {
         // ------------------------------------------------------------ epilogue
-        if constexpr (SPANS && TMA) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        if constexpr (SPANS) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // A block of NR rows: this lane has NR values of one c; for SwiGLU gate and up of every other row of one c.
         const int uh = (warp - 4) >> 2;
         const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -1026,7 +749,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 release(ab);
                 ++acc;
             } else if constexpr (SPANS) {   // spans summed in registers
-                constexpr int NU = TMA ? 8 : 2;   // units of this warp (the element loader's CTAs have BN <= 64)
+                constexpr int NU = 8;   // units of this warp
                 float v[NU][16];
 #pragma unroll
                 for (int i = 0; i < NU; ++i)
@@ -1118,17 +841,14 @@ inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether TMA can read the operands as they lie: 16-byte aligned bases, strides of whole 16 bytes.
-inline bool lt_tma_ok(const LinArgs& a) {
-    auto base = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-    const bool groups = a.kind != LIN_WGRAD && a.E > 1;
-    const long long far = 1LL << 30;   // rows up to 2 GB apart: 32-bit steps in the gather, strides a map can hold
-    return a.lda < far && a.ldb < far && base(a.a[0]) && base(a.a[1]) && base(a.b[0]) && base(a.b[1]) && a.lda % 8 == 0 && a.ldb % 8 == 0 &&
-           (!groups || a.a_gstride % 8 == 0);
+// Whether TMA can read a matrix as it lies: a 16-byte aligned base and strides of whole 16 bytes that a map can hold.
+inline bool lt_tma_ok(const void* p, long long ld, long long gstride) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && gstride % 8 == 0 && ld < (1LL << 36) &&
+           gstride < (1LL << 38);
 }
 
 // One candidate tile shape and what it is estimated to take, in SM cycles.
-inline double lt_shape(const LinArgs& a, bool tma, int cg, int split, int bn, const int* slots_of, int smem_limit,
+inline double lt_shape(const LinArgs& a, int cg, int split, int bn, const int* slots_of, int smem_limit,
                        LtPlan* p) {
     const bool dual = a.kind == LIN_FWD && a.a[1], wg = a.kind == LIN_WGRAD;
     *p = LtPlan{};
@@ -1178,7 +898,6 @@ inline double lt_shape(const LinArgs& a, bool tma, int cg, int split, int bn, co
     double stage = 2.0 * bn * fill;
     if (stage < bytes / 48) stage = bytes / 48;
     if (stage < (dual ? 560 : 480)) stage = dual ? 560 : 480;
-    if (!tma) stage = (kLtM + brows * fill) * 16;     // element by element
     const double rounds = a.E == 1 || wg ? static_cast<double>((static_cast<long long>(tiles) + slots - 1) / slots)
                                          : (tiles / slots > 1 ? tiles / slots + 0.5 : 1.0);
     const double tile = nkb / split * stage, out = 12.0 * bn * fill;   // out: the epilogue, hidden but for the last
@@ -1187,16 +906,15 @@ inline double lt_shape(const LinArgs& a, bool tma, int cg, int split, int bn, co
 }
 
 // The shape with the smallest estimate.  slots: how many clusters of n CTAs the GPU holds at a time, n = 1 .. 8.
-inline LtPlan lt_plan(const LinArgs& a, bool tma, const int* slots, int smem_limit) {
+inline LtPlan lt_plan(const LinArgs& a, const int* slots, int smem_limit) {
     LtPlan best{}, p;
     double least = -1;
     const int nkb = a.kind == LIN_WGRAD ? (a.rows / a.E + kLtBK - 1) / kLtBK
                                         : (a.Q + kLtBK - 1) / kLtBK * (a.kind == LIN_DGRAD && a.b[1] ? 2 : 1);
-    const int most = tma || a.out_type != LIN_F32 ? 256 : 64;
-    for (int cg = 1; cg <= (tma ? 2 : 1); ++cg)
-        for (int bn = (a.kind == LIN_WGRAD ? 64 : 16) * cg; bn <= most; bn *= 2)
+    for (int cg = 1; cg <= 2; ++cg)
+        for (int bn = (a.kind == LIN_WGRAD ? 64 : 16) * cg; bn <= 256; bn *= 2)
             for (int split = 1; split <= 8 && (split == 1 || (cg == 1 && split * 4 <= nkb)); ++split) {
-                const double t = lt_shape(a, tma, cg, split, bn, slots, smem_limit, &p);
+                const double t = lt_shape(a, cg, split, bn, slots, smem_limit, &p);
                 if (t < 0) continue;
                 if (least < 0 || t < least) {
                     least = t;
@@ -1208,13 +926,11 @@ inline LtPlan lt_plan(const LinArgs& a, bool tma, const int* slots, int smem_lim
 }
 
 inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
-    const uint64_t R = static_cast<uint64_t>(a.rows > 0 ? a.rows : 1);
     const uint64_t C = a.C, Q = a.Q, E = a.E, lda = a.lda, ldb = a.ldb;
-    const bool g = a.gather != nullptr;
+    const uint64_t R = static_cast<uint64_t>(a.b_rows > 0 ? a.b_rows : 1);   // rows of B (wgrad: of both)
     bool ok = true;
     if (a.kind == LIN_WGRAD) {   // A = x [rows, C], B = dz [rows, out_n]
-        const uint64_t xr = g ? a.gather_total : R;
-        ok = lt_encode(&m->a0, a.type, a.a[0], C, xr, 1, lda, lda * xr, 64) &&
+        ok = lt_encode(&m->a0, a.type, a.a[0], C, R, 1, lda, lda * R, 64) &&
              lt_encode(&m->b0, a.type, a.b[0], a.out_n, R, 1, ldb, ldb * R, 64);
         m->a1 = m->a0;
         m->b1 = m->b0;
@@ -1223,23 +939,22 @@ inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     const bool fwd = a.kind == LIN_FWD;
     const uint64_t inner = fwd ? Q : C, outer = fwd ? C : Q;
     const uint64_t gs = E > 1 ? static_cast<uint64_t>(a.a_gstride) : lda * outer;
-    const uint64_t br = g && fwd ? a.gather_total : R;
     const uint32_t abox = !fwd ? 64 : a.a[1] ? 16 : kLtM;
     ok = lt_encode(&m->a0, a.type, a.a[0], inner, outer, E, lda, gs, abox) &&
-         lt_encode(&m->b0, a.type, a.b[0], Q, br, 1, ldb, ldb * br, p.bbox);
+         lt_encode(&m->b0, a.type, a.b[0], Q, R, 1, ldb, ldb * R, p.bbox);
     m->a1 = m->a0;
     m->b1 = m->b0;
     if (a.a[1]) ok = ok && lt_encode(&m->a1, a.type, a.a[1], inner, outer, E, lda, gs, abox);
-    if (a.b[1]) ok = ok && lt_encode(&m->b1, a.type, a.b[1], Q, br, 1, ldb, ldb * br, p.bbox);
+    if (a.b[1]) ok = ok && lt_encode(&m->b1, a.type, a.b[1], Q, R, 1, ldb, ldb * R, p.bbox);
     return ok;
 }
 
 // Launch the kernel a plan asks for (a translation unit each: linear_fwd.cu, linear_swiglu.cu, linear_dgrad.cu,
 // linear_wgrad.cu).
-cudaError_t lin_launch_fwd(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
-cudaError_t lin_launch_swiglu(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
-cudaError_t lin_launch_dgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
-cudaError_t lin_launch_wgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s);
+cudaError_t lin_launch_fwd(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s);
+cudaError_t lin_launch_swiglu(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s);
+cudaError_t lin_launch_dgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s);
+cudaError_t lin_launch_wgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s);
 // Let the kernels of a direction use `bytes` of dynamic shared memory on the current device.
 cudaError_t lin_allow_fwd(int bytes);
 cudaError_t lin_allow_swiglu(int bytes);
@@ -1248,11 +963,11 @@ cudaError_t lin_allow_wgrad(int bytes);
 // How many clusters of n = 1 .. 8 CTAs of these kernels the current device holds at a time (slots[0] unused).
 cudaError_t lin_slots(int smem, int* slots);
 
-template <int KIND, bool DUAL, bool TMA, int CG, bool SPANS>
+template <int KIND, bool DUAL, int CG, bool SPANS>
 cudaError_t lt_launch_k(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(lt_threads(TMA)));
+    cfg.blockDim = dim3(static_cast<unsigned>(kLtThreads));
     cfg.dynamicSmemBytes = static_cast<size_t>(p.smem);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -1264,30 +979,26 @@ cudaError_t lt_launch_k(const LinArgs& a, const LtPlan& p, const LtMaps& m, cuda
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cg * p.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, lin_tc_kernel<KIND, DUAL, TMA, CG, SPANS>, a, p, m);
+    return cudaLaunchKernelEx(&cfg, lin_tc_kernel<KIND, DUAL, CG, SPANS>, a, p, m);
 }
 
 template <int KIND, bool DUAL, bool SPANS>
-cudaError_t lt_launch(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
-    if (!tma) return lt_launch_k<KIND, DUAL, false, 1, SPANS>(a, p, m, s);
-    return p.cg == 2 ? lt_launch_k<KIND, DUAL, true, 2, SPANS>(a, p, m, s)
-                     : lt_launch_k<KIND, DUAL, true, 1, SPANS>(a, p, m, s);
+cudaError_t lt_launch(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s) {
+    return p.cg == 2 ? lt_launch_k<KIND, DUAL, 2, SPANS>(a, p, m, s) : lt_launch_k<KIND, DUAL, 1, SPANS>(a, p, m, s);
 }
 
 template <int KIND, bool DUAL>
-cudaError_t lt_launch(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
-    return a.out_type == LIN_F32 ? lt_launch<KIND, DUAL, true>(a, p, m, tma, s)
-                                 : lt_launch<KIND, DUAL, false>(a, p, m, tma, s);
+cudaError_t lt_launch(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s) {
+    return a.out_type == LIN_F32 ? lt_launch<KIND, DUAL, true>(a, p, m, s)
+                                 : lt_launch<KIND, DUAL, false>(a, p, m, s);
 }
 
 template <int KIND, bool DUAL>
 cudaError_t lt_allow(int bytes) {
-    const void* k[] = {reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 1, false>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 2, false>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, false, 1, false>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 1, true>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, true, 2, true>),
-                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, false, 1, true>)};
+    const void* k[] = {reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, 1, false>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, 2, false>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, 1, true>),
+                       reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, 2, true>)};
     for (const void* f : k) {
         const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;

@@ -3,8 +3,8 @@
 
 namespace moe {
 
-cudaError_t lin_launch_wgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, bool tma, cudaStream_t s) {
-    return lt_launch<LIN_WGRAD, false>(a, p, m, tma, s);
+cudaError_t lin_launch_wgrad(const LinArgs& a, const LtPlan& p, const LtMaps& m, cudaStream_t s) {
+    return lt_launch<LIN_WGRAD, false>(a, p, m, s);
 }
 
 cudaError_t lin_allow_wgrad(int bytes) { return lt_allow<LIN_WGRAD, false>(bytes); }

@@ -17,6 +17,7 @@
 #include "decode_common.cuh"
 #include "decode_mx.cuh"
 #include "linear_grad.cuh"
+#include "linear_pack.cuh"
 #include "linear_tc.cuh"
 #include "router.cuh"
 #include "slot_layout.cuh"
@@ -924,11 +925,10 @@ int64_t lin_gs(int64_t gs, int64_t rows, int64_t ld, int64_t width) {
 }
 
 cudaError_t lin_run(moe_fp4_ctx* c, const char* name, const LinArgs& a, cudaStream_t s) {
-    const bool tma = lt_tma_ok(a);
-    const LtPlan p = lt_plan(a, tma, c->lin_slots, c->smem_optin);
+    const LtPlan p = lt_plan(a, c->lin_slots, c->smem_optin);
     if (p.grid < 1) return cudaErrorInvalidConfiguration;
     LtMaps m{};
-    if (tma && !lt_maps(a, p, &m)) return cudaErrorInvalidValue;
+    if (!lt_maps(a, p, &m)) return cudaErrorInvalidValue;
     const bool prof = c->profile && c->prof.size() < 65536;
     cudaEvent_t ea = nullptr, eb = nullptr;
     if (prof) {
@@ -936,10 +936,10 @@ cudaError_t lin_run(moe_fp4_ctx* c, const char* name, const LinArgs& a, cudaStre
         eb = take_event(c);
         cudaEventRecord(ea, s);
     }
-    const cudaError_t e = a.kind == LIN_DGRAD   ? lin_launch_dgrad(a, p, m, tma, s)
-                          : a.kind == LIN_WGRAD ? lin_launch_wgrad(a, p, m, tma, s)
-                          : a.a[1]              ? lin_launch_swiglu(a, p, m, tma, s)
-                                                : lin_launch_fwd(a, p, m, tma, s);
+    const cudaError_t e = a.kind == LIN_DGRAD   ? lin_launch_dgrad(a, p, m, s)
+                          : a.kind == LIN_WGRAD ? lin_launch_wgrad(a, p, m, s)
+                          : a.a[1]              ? lin_launch_swiglu(a, p, m, s)
+                                                : lin_launch_fwd(a, p, m, s);
     if (prof) {
         cudaEventRecord(eb, s);
         c->prof.push_back({name, ea, eb});
@@ -947,12 +947,103 @@ cudaError_t lin_run(moe_fp4_ctx* c, const char* name, const LinArgs& a, cudaStre
     return e;
 }
 
+// Where a call's copies lie in its scratch.
+struct LinScratch {
+    size_t bytes = 0;
+    size_t take(long long rows, long long ld) {
+        const size_t at = bytes;
+        bytes += (static_cast<size_t>(rows) * static_cast<size_t>(ld) * 2 + 255) / 256 * 256;
+        return at;
+    }
+};
+int64_t lin_padded(int64_t width) { return (width + 7) / 8 * 8; }
+uint16_t* lin_at(void* scratch, size_t at) { return reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(scratch) + at); }
+
+// The copies a call makes: x (gathered, packed or aligned) and weights that TMA cannot read.
+struct LinCopies {
+    bool x = false, w = false, packed = false;   // packed: x and dz
+    size_t x_at = 0, w_at[2] = {0, 0};
+    long long x_rows = 0;                         // rows of the copy of x
+};
+
+LinCopies lin_forward_copies(const moe_fp4_linear_args* p, LinScratch* z) {
+    LinCopies k;
+    const int64_t K = p->in_features, N = p->out_features, ldw = lin_ld(p->ldw, K), ldx = lin_ld(p->ldx, K);
+    const int64_t gs = p->n_groups > 1 ? lin_gs(p->w_group_stride, N, ldw, K) : 0, E = p->n_groups ? p->n_groups : 1;
+    k.x = p->x_rows || !lt_tma_ok(p->x, ldx, 0);
+    k.w = !lt_tma_ok(p->w, ldw, gs) || (p->w_up && !lt_tma_ok(p->w_up, ldw, gs));
+    k.x_rows = p->rows;
+    if (k.x) k.x_at = z->take(p->rows, lin_padded(K));
+    if (k.w) k.w_at[0] = z->take(E * N, lin_padded(K));
+    if (k.w && p->w_up) k.w_at[1] = z->take(E * N, lin_padded(K));
+    return k;
+}
+
+struct LinGradPlan {
+    LinCopies k;
+    bool direct;                      // dy serves as dz
+    size_t dz_at[2] = {0, 0};
+    long long dz_rows;
+};
+
+LinGradPlan lin_backward_copies(const moe_fp4_linear_grads* p, LinScratch* z) {
+    LinGradPlan g;
+    LinCopies& k = g.k;
+    const int64_t K = p->in_features, N = p->out_features, ldw = lin_ld(p->ldw, K), ldx = lin_ld(p->ldx, K);
+    const int64_t gs = p->n_groups > 1 ? lin_gs(p->w_group_stride, N, ldw, K) : 0, E = p->n_groups ? p->n_groups : 1;
+    const bool want_dw = p->dw || p->dw_up, gated = p->act == MOE_FP4_ACT_SWIGLU;
+    k.packed = p->n_groups > 0 && want_dw;
+    k.x = want_dw && (k.packed || p->x_rows || !lt_tma_ok(p->x, ldx, 0));
+    k.w = p->dx && (!lt_tma_ok(p->w, ldw, gs) || (p->w_up && !lt_tma_ok(p->w_up, ldw, gs)));
+    g.dz_rows = k.x_rows = k.packed ? lin_packed_rows(p->rows, E) : p->rows;
+    g.direct = p->act == MOE_FP4_ACT_NONE && p->dy_type == p->type && !p->y_rows && !k.packed &&
+               lt_tma_ok(p->dy, lin_ld(p->lddy, N), 0);
+    if (!g.direct && (want_dw || p->dx)) {
+        g.dz_at[0] = z->take(g.dz_rows, lin_padded(N));
+        if (gated) g.dz_at[1] = z->take(g.dz_rows, lin_padded(N));
+    }
+    if (k.x) k.x_at = z->take(k.x_rows, lin_padded(K));
+    if (k.w) k.w_at[0] = z->take(E * N, lin_padded(K));
+    if (k.w && gated) k.w_at[1] = z->take(E * N, lin_padded(K));
+    return g;
+}
+
+// Make the copies of x and the weights.
+cudaError_t lin_pack(moe_fp4_ctx* c, const LinCopies& k, void* scratch, const int32_t* offsets, int E, int rows, int K,
+                     int N, const void* x, int64_t ldx, const int32_t* x_rows, int x_total, const void* w,
+                     const void* w_up, int64_t ldw, int64_t gs, cudaStream_t s) {
+    LinPackArgs a{};
+    a.offsets = offsets;
+    a.E = E;
+    a.rows = rows;
+    a.packed = k.packed;
+    a.index = x_rows;
+    a.total = x_rows ? x_total : rows;
+    a.err = c->d_err;
+    int n = 0;
+    long long blocks = 0;
+    auto job = [&](const void* src, size_t at, int64_t lds, int64_t gstride, int64_t per_group, long long b) {
+        a.job[n++] = LinPackJob{static_cast<const uint16_t*>(src), lin_at(scratch, at), lds, lin_padded(K), gstride, K,
+                                static_cast<int>(per_group)};
+        if (b > blocks) blocks = b;
+    };
+    if (k.x) job(x, k.x_at, ldx, 0, 0, (k.x_rows + kLpRows - 1) / kLpRows);
+    const long long wb = static_cast<long long>(E) * ((N + kLpRows - 1) / kLpRows);
+    if (k.w) job(w, k.w_at[0], ldw, gs, N, wb);
+    if (k.w && w_up) job(w_up, k.w_at[1], ldw, gs, N, wb);
+    const long long cols = (lin_padded(K) + kLpCols - 1) / kLpCols;
+    if (blocks > 0x7FFFFFFF || cols > 65535) return cudaErrorInvalidConfiguration;
+    return launch_k(c, "linear_pack", lin_pack_kernel,
+                    dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(cols), static_cast<unsigned>(n)),
+                    dim3(kLpThreads), 0, s, a);
+}
+
 cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
-    const bool db = g.db[0] || g.db[1];
+    const bool db = g.db[0] || g.db[1], by_group = db || g.packed;
     // Strips of rows.  With db those of a group form a cluster (8 CTAs at most) and should hold enough rows for the
-    // meeting of their sums to be small beside the loads; without it 64 rows a strip keep every SM loading.
-    const int per_group = (g.rows + g.E - 1) / g.E;
-    int strips = db ? per_group / 256 : (g.rows + 63) / 64;
+    // meeting of their sums to be small beside the loads; else 64 rows a strip keep every SM loading.
+    const int per_group = by_group ? (g.rows + g.E - 1) / g.E : g.rows;
+    int strips = db ? per_group / 128 : (per_group + 63) / 64;
     const int most = db ? 8 : 65535;
     strips = strips < 1 ? 1 : strips > most ? most : strips;
     auto vec_ok = [](const void* p, long long ld, int type) {
@@ -963,7 +1054,7 @@ cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
                vec_ok(g.dz[1], g.lddz, g.type) && vec_ok(g.z[0], g.ldz, g.type) && vec_ok(g.z[1], g.ldz, g.type);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((g.N + kLgCols - 1) / kLgCols), static_cast<unsigned>(strips),
-                       static_cast<unsigned>(db ? g.E : 1));
+                       static_cast<unsigned>(by_group ? g.E : 1));
     cfg.blockDim = dim3(kLgThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -996,6 +1087,20 @@ cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
 
 }  // namespace
 
+extern "C" size_t moe_fp4_linear_scratch(const moe_fp4_linear_args* p) {
+    if (!p || p->rows <= 0 || p->in_features < 1 || p->out_features < 1 || p->n_groups < 0) return 0;
+    LinScratch z;
+    lin_forward_copies(p, &z);
+    return z.bytes;
+}
+
+extern "C" size_t moe_fp4_linear_backward_scratch(const moe_fp4_linear_grads* p) {
+    if (!p || p->rows <= 0 || p->in_features < 1 || p->out_features < 1 || p->n_groups < 0) return 0;
+    LinScratch z;
+    lin_backward_copies(p, &z);
+    return z.bytes;
+}
+
 extern "C" moe_fp4_status moe_fp4_linear(moe_fp4_ctx* c, const moe_fp4_linear_args* p, void* stream) {
     if (!c) return MOE_FP4_EINVAL;
     if (!p) return host_fail(c, MOE_FP4_EINVAL, "linear: NULL arguments");
@@ -1027,6 +1132,18 @@ extern "C" moe_fp4_status moe_fp4_linear(moe_fp4_ctx* c, const moe_fp4_linear_ar
         return host_fail(c, MOE_FP4_EINVAL, "linear: a pointer is not aligned to its element");
     DeviceScope dev(c->device);
     if (!dev.ok) return host_fail(c, MOE_FP4_ECUDA, "linear: device %d", c->device);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    LinScratch z;
+    const LinCopies k = lin_forward_copies(p, &z);
+    if (z.bytes > 0) {
+        if (p->scratch_bytes < static_cast<int64_t>(z.bytes) || !p->scratch ||
+            (reinterpret_cast<uintptr_t>(p->scratch) & 15))
+            return host_fail(c, MOE_FP4_EINVAL, "linear: needs %zu bytes of 16-byte aligned scratch", z.bytes);
+        e = lin_pack(c, k, p->scratch, p->offsets, p->n_groups ? p->n_groups : 1, p->rows, K, N, p->x, ldx, p->x_rows,
+                     p->x_total, p->w, p->w_up, ldw, gs, s);
+        if (e != cudaSuccess) return cuda_fail(c, e, "linear: copy launch");
+    }
     LinArgs a{};
     a.offsets = p->offsets;
     a.E = p->n_groups ? p->n_groups : 1;
@@ -1036,14 +1153,13 @@ extern "C" moe_fp4_status moe_fp4_linear(moe_fp4_ctx* c, const moe_fp4_linear_ar
     a.kind = LIN_FWD;
     a.type = p->type;
     a.act = p->act;
-    a.a[0] = p->w;
-    a.a[1] = p->w_up;
-    a.lda = ldw;
-    a.a_gstride = gs;
-    a.b[0] = p->x;
-    a.ldb = ldx;
-    a.gather = p->x_rows;
-    a.gather_total = p->x_rows ? p->x_total : p->rows;
+    a.a[0] = k.w ? lin_at(p->scratch, k.w_at[0]) : p->w;
+    a.a[1] = k.w && p->w_up ? lin_at(p->scratch, k.w_at[1]) : p->w_up;
+    a.lda = k.w ? lin_padded(K) : ldw;
+    a.a_gstride = k.w ? N * lin_padded(K) : gs;
+    a.b[0] = k.x ? lin_at(p->scratch, k.x_at) : p->x;
+    a.ldb = k.x ? lin_padded(K) : ldx;
+    a.b_rows = p->rows;
     a.out[0] = p->y;
     a.ldo = ldy;
     a.out_type = p->y_type;
@@ -1060,7 +1176,7 @@ extern "C" moe_fp4_status moe_fp4_linear(moe_fp4_ctx* c, const moe_fp4_linear_ar
     a.ldz = ldz;
     a.err = c->d_err;
     a.timeout_ns = c->timeout_ns;
-    const cudaError_t e = lin_run(c, "linear", a, static_cast<cudaStream_t>(stream));
+    e = lin_run(c, "linear", a, s);
     return e == cudaSuccess ? MOE_FP4_OK : cuda_fail(c, e, "linear: launch");
 }
 
@@ -1075,31 +1191,26 @@ extern "C" moe_fp4_status moe_fp4_linear_backward(moe_fp4_ctx* c, const moe_fp4_
     if ((p->dy_type != p->type && p->dy_type != MOE_FP4_F32) || (p->dx && !lin_type_any(p->dx_type)) ||
         ((p->dw || p->dw_up) && !lin_type_any(p->dw_type)) || p->reserved)
         return host_fail(c, MOE_FP4_EINVAL, "linear_backward: dy has the type of x or fp32; unknown dx or dw type");
-    if (!gated && (p->w_up || p->dw_up || p->db_up || p->dz_up || p->z_up))
+    if (!gated && (p->w_up || p->dw_up || p->db_up || p->z_up))
         return host_fail(c, MOE_FP4_EINVAL, "linear_backward: *_up tensors go with ACT_SWIGLU");
     const int64_t lddy = lin_ld(p->lddy, N), ldz = lin_ld(p->ldz, N), ldx = lin_ld(p->ldx, K), ldw = lin_ld(p->ldw, K),
-                  lddz = lin_ld(p->lddz, N), lddx = lin_ld(p->lddx, K), lddw = lin_ld(p->lddw, K);
+                  lddx = lin_ld(p->lddx, K), lddw = lin_ld(p->lddw, K);
     const int64_t gs = p->n_groups ? lin_gs(p->w_group_stride, N, ldw, K) : 0;
     const int64_t dgs = p->n_groups ? lin_gs(p->dw_group_stride, N, lddw, K) : 0;
-    if (lddy < 0 || ldz < 0 || ldx < 0 || ldw < 0 || lddz < 0 || lddx < 0 || lddw < 0 || gs < 0 || dgs < 0)
+    if (lddy < 0 || ldz < 0 || ldx < 0 || ldw < 0 || lddx < 0 || lddw < 0 || gs < 0 || dgs < 0)
         return host_fail(c, MOE_FP4_EINVAL, "linear_backward: a stride is smaller than what it steps over");
     const bool want_dx = p->dx && R > 0, want_dw = p->dw || p->dw_up, want_db = p->db || p->db_up;
-    const bool direct = plain && p->dy_type == p->type && !p->y_rows;   // dy serves as dz
     if (R > 0) {
         if (!p->dy) return host_fail(c, MOE_FP4_EINVAL, "linear_backward: NULL dy");
         if (!plain && (!p->z || (gated && !p->z_up))) return host_fail(c, MOE_FP4_EINVAL, "linear_backward: NULL z");
         if (want_dx && (!p->w || (gated && !p->w_up))) return host_fail(c, MOE_FP4_EINVAL, "linear_backward: NULL w");
         if (want_dw && !p->x) return host_fail(c, MOE_FP4_EINVAL, "linear_backward: NULL x");
-        if (!direct && (want_dx || p->dw) && !p->dz)
-            return host_fail(c, MOE_FP4_EINVAL, "linear_backward: dz is needed here");
-        if (gated && (want_dx || p->dw_up) && !p->dz_up)
-            return host_fail(c, MOE_FP4_EINVAL, "linear_backward: dz_up is needed here");
         if ((p->x_rows && p->x_total < 1) || (p->y_rows && p->y_total < 1) || (p->dx_rows && p->dx_total < 1))
             return host_fail(c, MOE_FP4_EINVAL, "linear_backward: x_rows, y_rows and dx_rows need their totals");
     }
     if (!lin_aligned(p->dy, p->dy_type) || !lin_aligned(p->z, p->type) || !lin_aligned(p->z_up, p->type) ||
         !lin_aligned(p->x, p->type) || !lin_aligned(p->w, p->type) || !lin_aligned(p->w_up, p->type) ||
-        !lin_aligned(p->dz, p->type) || !lin_aligned(p->dz_up, p->type) || !lin_aligned(p->dx, p->dx_type) ||
+        !lin_aligned(p->dx, p->dx_type) ||
         !lin_aligned(p->dw, p->dw_type) || !lin_aligned(p->dw_up, p->dw_type) || !lin_aligned(p->db, MOE_FP4_F32) ||
         !lin_aligned(p->db_up, MOE_FP4_F32) || !lin_aligned(p->x_rows, MOE_FP4_F32) ||
         !lin_aligned(p->y_rows, MOE_FP4_F32) || !lin_aligned(p->dx_rows, MOE_FP4_F32))
@@ -1109,39 +1220,55 @@ extern "C" moe_fp4_status moe_fp4_linear_backward(moe_fp4_ctx* c, const moe_fp4_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     const int E = p->n_groups ? p->n_groups : 1;
-    if ((!direct && (p->dz || p->dz_up) && R > 0) || want_db) {
-        LinGradArgs g{};
-        g.offsets = p->offsets;
-        g.E = E;
-        g.rows = R;
-        g.N = N;
-        g.type = p->type;
-        g.act = p->act;
-        g.dy_rows = p->y_rows;
-        g.dy_total = p->y_rows ? p->y_total : R;
-        g.dy_type = p->dy_type;
-        g.dy = p->dy;
-        g.lddy = lddy;
-        g.z[0] = plain ? nullptr : p->z;
-        g.z[1] = p->z_up;
-        g.ldz = ldz;
-        g.dz[0] = p->dz;
-        g.dz[1] = p->dz_up;
-        g.lddz = lddz;
-        g.db[0] = p->db;
-        g.db[1] = p->db_up;
-        g.accumulate = p->accumulate;
-        g.err = c->d_err;
-        if ((e = lin_grad_run(c, g, s)) != cudaSuccess) return cuda_fail(c, e, "linear_backward: dz launch");
+    LinScratch z;
+    const LinGradPlan g = lin_backward_copies(p, &z);
+    const LinCopies& k = g.k;
+    if (R > 0 && z.bytes > 0 &&
+        (p->scratch_bytes < static_cast<int64_t>(z.bytes) || !p->scratch ||
+         (reinterpret_cast<uintptr_t>(p->scratch) & 15)))
+        return host_fail(c, MOE_FP4_EINVAL, "linear_backward: needs %zu bytes of 16-byte aligned scratch", z.bytes);
+    if (R > 0 && (k.x || k.w)) {
+        e = lin_pack(c, k, p->scratch, p->offsets, E, R, K, N, p->x, ldx, p->x_rows, p->x_total, p->w, p->w_up, ldw, gs,
+                     s);
+        if (e != cudaSuccess) return cuda_fail(c, e, "linear_backward: copy launch");
+    }
+    const bool need_dz = !g.direct && (want_dx || want_dw) && R > 0;
+    if (need_dz || want_db) {
+        LinGradArgs d{};
+        d.offsets = p->offsets;
+        d.E = E;
+        d.rows = R;
+        d.N = N;
+        d.type = p->type;
+        d.act = p->act;
+        d.dy_rows = p->y_rows;
+        d.dy_total = p->y_rows ? p->y_total : R;
+        d.dy_type = p->dy_type;
+        d.dy = p->dy;
+        d.lddy = lddy;
+        d.z[0] = plain ? nullptr : p->z;
+        d.z[1] = p->z_up;
+        d.ldz = ldz;
+        d.dz[0] = need_dz ? lin_at(p->scratch, g.dz_at[0]) : nullptr;
+        d.dz[1] = need_dz && gated ? lin_at(p->scratch, g.dz_at[1]) : nullptr;
+        d.lddz = lin_padded(N);
+        d.packed = need_dz && k.packed;
+        d.db[0] = p->db;
+        d.db[1] = p->db_up;
+        d.accumulate = p->accumulate;
+        d.err = c->d_err;
+        if ((e = lin_grad_run(c, d, s)) != cudaSuccess) return cuda_fail(c, e, "linear_backward: dz launch");
     }
     LinArgs a{};
     a.offsets = p->offsets;
     a.E = E;
     a.rows = R;
     a.type = p->type;
-    a.b[0] = direct ? p->dy : p->dz;
-    a.b[1] = p->dz_up;
-    a.ldb = direct ? lddy : lddz;
+    a.b[0] = g.direct ? p->dy : R > 0 ? lin_at(p->scratch, g.dz_at[0]) : nullptr;
+    a.b[1] = gated && R > 0 ? lin_at(p->scratch, g.dz_at[1]) : nullptr;
+    a.ldb = g.direct ? lddy : lin_padded(N);
+    a.b_rows = static_cast<int>(g.direct ? R : g.dz_rows);
+    a.packed = k.packed;
     a.C = K;
     a.err = c->d_err;
     a.timeout_ns = c->timeout_ns;
@@ -1149,10 +1276,10 @@ extern "C" moe_fp4_status moe_fp4_linear_backward(moe_fp4_ctx* c, const moe_fp4_
         LinArgs d = a;
         d.kind = LIN_DGRAD;
         d.Q = N;
-        d.a[0] = p->w;
-        d.a[1] = p->w_up;
-        d.lda = ldw;
-        d.a_gstride = gs;
+        d.a[0] = k.w ? lin_at(p->scratch, k.w_at[0]) : p->w;
+        d.a[1] = !gated ? nullptr : k.w ? lin_at(p->scratch, k.w_at[1]) : p->w_up;
+        d.lda = k.w ? lin_padded(K) : ldw;
+        d.a_gstride = k.w ? N * lin_padded(K) : gs;
         d.out[0] = p->dx;
         d.ldo = lddx;
         d.out_type = p->dx_type;
@@ -1160,18 +1287,28 @@ extern "C" moe_fp4_status moe_fp4_linear_backward(moe_fp4_ctx* c, const moe_fp4_
         d.scatter_total = p->dx_rows ? p->dx_total : R;
         if ((e = lin_run(c, "linear_dx", d, s)) != cudaSuccess) return cuda_fail(c, e, "linear_backward: dx launch");
     }
-    if (want_dw) {
+    if (want_dw && R == 0) {   // every group is empty: no sums to run
+        if (!p->accumulate) {
+            for (void* t : {p->dw, p->dw_up}) {
+                const size_t width = static_cast<size_t>(K) * (p->dw_type == MOE_FP4_F32 ? 4 : 2);
+                for (int i = 0; t && i < E; ++i) {
+                    const size_t es = p->dw_type == MOE_FP4_F32 ? 4 : 2;
+                    e = cudaMemset2DAsync(static_cast<uint8_t*>(t) + static_cast<size_t>(i) * dgs * es,
+                                          static_cast<size_t>(lddw) * es, 0, width, static_cast<size_t>(N), s);
+                    if (e != cudaSuccess) return cuda_fail(c, e, "linear_backward: dw");
+                }
+            }
+        }
+    } else if (want_dw) {
         LinArgs d = a;
         d.kind = LIN_WGRAD;
         d.out_n = N;
-        d.a[0] = p->x;
-        d.lda = ldx;
-        d.gather = p->x_rows;
-        d.gather_total = p->x_rows ? p->x_total : R;
+        d.a[0] = k.x ? lin_at(p->scratch, k.x_at) : p->x;
+        d.lda = k.x ? lin_padded(K) : ldx;
         d.out[0] = p->dw;
         d.out[1] = p->dw_up;
         if (!p->dw) {   // only the second weight's gradient
-            d.b[0] = p->dz_up;
+            d.b[0] = d.b[1];
             d.out[0] = p->dw_up;
         }
         if (!p->dw || !p->dw_up) d.b[1] = nullptr;

@@ -26,7 +26,8 @@ EXPORTS = ("moe_fp4_slot_bytes", "moe_fp4_create", "moe_fp4_destroy", "moe_fp4_a
            "moe_fp4_set_option", "moe_fp4_profile_read", "moe_fp4_load_expert_slot", "moe_fp4_route",
            "moe_fp4_forward", "moe_fp4_route_forward", "moe_fp4_last_error", "moe_fp4_forward_noalloc",
            "moe_fp4_saliency", "moe_fp4_stream_experts", "moe_fp4_residency_stats", "moe_fp4_expert_outputs",
-           "moe_fp4_combine", "moe_fp4_linear", "moe_fp4_linear_backward")
+           "moe_fp4_combine", "moe_fp4_linear", "moe_fp4_linear_backward", "moe_fp4_linear_scratch",
+           "moe_fp4_linear_backward_scratch")
 
 # element types and activations of the 16-bit products (moe_fp4_linear)
 BF16, F16, F32 = 0, 1, 2
@@ -60,7 +61,8 @@ class LinearArgs(ctypes.Structure):
         [(n, ctypes.c_int32) for n in ("bias_type", "residual_type")] + \
         [("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("y", ctypes.c_void_p),
          ("ldy", ctypes.c_int64), ("y_type", ctypes.c_int32), ("reserved", ctypes.c_int32),
-         ("z", ctypes.c_void_p), ("z_up", ctypes.c_void_p), ("ldz", ctypes.c_int64)]
+         ("z", ctypes.c_void_p), ("z_up", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+         ("scratch", ctypes.c_void_p), ("scratch_bytes", ctypes.c_int64)]
 
 
 class LinearGradArgs(ctypes.Structure):
@@ -72,11 +74,12 @@ class LinearGradArgs(ctypes.Structure):
          ("ldz", ctypes.c_int64)] + \
         [(n, ctypes.c_void_p) for n in ("x", "w", "w_up")] + \
         [(n, ctypes.c_int64) for n in ("ldx", "ldw", "w_group_stride")] + \
-        [("dz", ctypes.c_void_p), ("dz_up", ctypes.c_void_p), ("lddz", ctypes.c_int64), ("dx", ctypes.c_void_p),
+        [("dx", ctypes.c_void_p),
          ("lddx", ctypes.c_int64), ("dx_type", ctypes.c_int32), ("dw_type", ctypes.c_int32),
          ("dw", ctypes.c_void_p), ("dw_up", ctypes.c_void_p), ("lddw", ctypes.c_int64),
          ("dw_group_stride", ctypes.c_int64), ("db", ctypes.c_void_p), ("db_up", ctypes.c_void_p),
-         ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+         ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32), ("scratch", ctypes.c_void_p),
+         ("scratch_bytes", ctypes.c_int64)]
 
 
 @dataclass
@@ -137,6 +140,10 @@ def load(path: str = LIB_PATH):
         L.moe_fp4_forward_noalloc.argtypes = [ctypes.POINTER(Config), P, P, I32, P, I32, P, P, P, P, P, P, P]
         L.moe_fp4_linear.restype = I32
         L.moe_fp4_linear.argtypes = [P, ctypes.POINTER(LinearArgs), P]
+        L.moe_fp4_linear_scratch.restype = SZ
+        L.moe_fp4_linear_scratch.argtypes = [ctypes.POINTER(LinearArgs)]
+        L.moe_fp4_linear_backward_scratch.restype = SZ
+        L.moe_fp4_linear_backward_scratch.argtypes = [ctypes.POINTER(LinearGradArgs)]
         L.moe_fp4_linear_backward.restype = I32
         L.moe_fp4_linear_backward.argtypes = [P, ctypes.POINTER(LinearGradArgs), P]
         _lib = L
@@ -471,8 +478,9 @@ class Context:
                            None if offsets is None else offsets.data_ptr(), pxr, pyr, x_total, y_total, px, pw, pu,
                            ldx, ldw, gs, pb, pbu, bt, rt, pr, ldr, py, ldy, _TYPES[y.dtype], 0,
                            None if z is None else z.data_ptr(), None if z_up is None else z_up.data_ptr(), N)
+            scratch = chk.scratch(a, self.lib.moe_fp4_linear_scratch, x.device)
             if other is not None:
-                chk.keep(other, x, w, w_up, offsets, bias, bias_up, residual, x_rows, y_rows, y, z, z_up)
+                chk.keep(other, x, w, w_up, offsets, bias, bias_up, residual, x_rows, y_rows, y, z, z_up, scratch)
             rc = self.lib.moe_fp4_linear(self.h, ctypes.byref(a), s)
             if rc != OK:
                 self._check(rc, what)
@@ -558,7 +566,6 @@ class Context:
         pyr = None if y_rows is None else chk.index(y_rows, "y_rows", R)
         pdr = None if dx_rows is None else chk.index(dx_rows, "dx_rows", R)
         t16 = _PLAIN[x.dtype]
-        need_dz = (act_id != 0 or dyt == F32 or y_rows is not None) and (need_dx or need_dw)
 
         def call(s, other, dx, dw, dw_up, db, db_up):
             def new(shape, dtype):
@@ -566,8 +573,6 @@ class Context:
 
             pdx = pdw = pdwu = pdb = pdbu = None
             lddx = lddw = dgs = dxt = dwt = 0
-            dz = new((R, N), t16) if need_dz else None
-            dz_up = new((R, N), t16) if need_dz and two else None
             if need_dx:
                 dx = new((dx_total, K), t16) if dx is None else dx
                 pdx, lddx = chk.matrix(dx, "dx", dx_total, K)
@@ -594,11 +599,11 @@ class Context:
             a = LinearGradArgs(R, K, N, wdt, act_id, 0 if offsets is None else E,
                                None if offsets is None else offsets.data_ptr(), pxr, pyr, pdr, x_total, dy_total,
                                dx_total, dyt, pdy, lddy, pz, pzu, ldz, px, pw, pu, ldx, ldw, gs,
-                               None if dz is None else dz.data_ptr(), None if dz_up is None else dz_up.data_ptr(), N,
                                pdx, lddx, dxt, dwt, pdw, pdwu, lddw, dgs, pdb, pdbu, int(accumulate), 0)
+            scratch = chk.scratch(a, self.lib.moe_fp4_linear_backward_scratch, x.device)
             if other is not None:
-                chk.keep(other, dy, x, w, w_up, offsets, z, z_up, x_rows, y_rows, dx_rows, dz, dz_up, dx, dw, dw_up, db,
-                         db_up)
+                chk.keep(other, dy, x, w, w_up, offsets, z, z_up, x_rows, y_rows, dx_rows, dx, dw, dw_up, db, db_up,
+                         scratch)
             rc = self.lib.moe_fp4_linear_backward(self.h, ctypes.byref(a), s)
             if rc != OK:
                 self._check(rc, what)
@@ -710,6 +715,16 @@ class _Check:
                 self.fail(f"the stream is not one of the context's device {self.dev}")
             with torch.cuda.stream(stream):
                 return call(stream.cuda_stream, stream, *outputs)
+
+    @staticmethod
+    def scratch(a, size, device):
+        """The scratch a call needs, if any, from torch's allocator (so it follows the call's stream)."""
+        n = size(ctypes.byref(a))
+        if n == 0:
+            return None
+        t = torch.empty(n, dtype=torch.uint8, device=device)
+        a.scratch, a.scratch_bytes = t.data_ptr(), n
+        return t
 
     @staticmethod
     def keep(s, *tensors):

@@ -433,6 +433,8 @@ typedef struct {
     int32_t reserved;          /* 0 */
     void *z, *z_up;            /* [R, N] out or NULL: pre-activations in grouped order, for the backward pass */
     int64_t ldz;
+    void *scratch;             /* at least moe_fp4_linear_scratch(args) bytes, 16-byte aligned (NULL if that is 0) */
+    int64_t scratch_bytes;
 } moe_fp4_linear_args;
 
 /*
@@ -450,15 +452,19 @@ typedef struct {
  * x_rows and y_rows fuse the gather of token rows into grouped order and the
  * scatter of results into entry order ((offsets, perm) of moe_fp4_route:
  * x_rows = perm / k, y_rows = perm).
- * Any size, row stride and (natural) alignment is accepted.  The fast operand
- * path needs x and w with 16-byte aligned bases and row strides that are
- * multiples of 8 elements.
- * No workspace is used: calls may overlap in time on different streams.
- * Errors: EINVAL, ECUDA; latched: EINVAL (offsets that do not ascend inside
- * [0, R]: that group is skipped; an x_rows entry outside [0, x_total): that
- * row counts as zero; a y_rows entry outside [0, y_total): that row is not
- * written), ETIMEOUT.
+ * Any size, row stride and (natural) alignment is accepted.  The tensor cores'
+ * loads need 16-byte aligned bases and row strides of whole 16 bytes; gathered
+ * rows, and x or weights that are not so, are first copied into `scratch`
+ * (weights only of groups that have rows).  moe_fp4_linear_scratch says how
+ * many bytes that takes, from sizes, pointers and strides alone; scratch must
+ * stay untouched until the call's work on `stream` is done.  Nothing else is
+ * shared, so calls with scratch of their own may overlap in time.
+ * Errors: EINVAL, ECUDA; latched: EINVAL (a group that is no part of [0, R] is
+ * skipped -- when offsets descend anywhere no result is valid; an x_rows entry
+ * outside [0, x_total): that row counts as zero; a y_rows entry outside
+ * [0, y_total): that row is not written), ETIMEOUT.
  */
+size_t moe_fp4_linear_scratch(const moe_fp4_linear_args *args);
 moe_fp4_status moe_fp4_linear(moe_fp4_ctx *ctx, const moe_fp4_linear_args *args, void *stream);
 
 /* Arguments of moe_fp4_linear_backward (zero the struct first; strides as above). */
@@ -477,10 +483,6 @@ typedef struct {
     int64_t ldz;
     const void *x, *w, *w_up;
     int64_t ldx, ldw, w_group_stride;
-    void *dz, *dz_up;          /* [R, N] out in `type`: the gradients before the activation, rounded once; dz may
-                                  be NULL when act is NONE, dy has type `type` and no y_rows are given (dy is
-                                  used as it is); dz_up for SWIGLU only */
-    int64_t lddz;
     void *dx;                  /* [dx_total (or R), K] out or NULL */
     int64_t lddx;
     int32_t dx_type;           /* MOE_FP4_BF16, _F16 or _F32 */
@@ -490,6 +492,8 @@ typedef struct {
     float *db, *db_up;         /* [N] or [E, N] out or NULL */
     int32_t accumulate;        /* nonzero: add to dw, dw_up, db, db_up instead of overwriting them */
     int32_t reserved;          /* 0 */
+    void *scratch;             /* at least moe_fp4_linear_backward_scratch(args) bytes, 16-byte aligned */
+    int64_t scratch_bytes;
 } moe_fp4_linear_grads;
 
 /*
@@ -499,11 +503,15 @@ typedef struct {
  *   db = sum over rows of dz (before its rounding, fp32, fixed order).
  * dw and db of an empty group are zero (unchanged with `accumulate`).  With
  * x_rows the gradient of a shared x row is the sum of its rows of dx, which
- * dx_rows = perm puts where moe_fp4_combine adds them up.  dz and dz_up are
- * the caller's buffers, so calls may overlap in time like moe_fp4_linear's.
- * Rows outside every group are neither read nor written.
+ * dx_rows = perm puts where moe_fp4_combine adds them up.  Rows outside every
+ * group are neither read nor written.  scratch holds dz and dz_up, rounded once
+ * to `type` (for ACT_NONE without y_rows and groups an aligned dy of type `type`
+ * is used as it is), and copies of x and w as in the forward; with groups the
+ * rows of dz and x lie there with zeros between the groups, which the sums over
+ * rows run into.
  * Errors: as moe_fp4_linear (a bad y_rows entry counts as a zero dy row).
  */
+size_t moe_fp4_linear_backward_scratch(const moe_fp4_linear_grads *args);
 moe_fp4_status moe_fp4_linear_backward(moe_fp4_ctx *ctx, const moe_fp4_linear_grads *args, void *stream);
 
 #ifdef __cplusplus
