@@ -46,6 +46,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "linear_common.cuh"
 #include "tma.cuh"
 #include "umma.cuh"
@@ -721,6 +723,105 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     else send(un, v);
                 }
             };
+            // The short way for the common outputs (no residual, no z, 16-bit in pairs or fp32): what a value's way out
+            // depends on is known here at compile time.  The general way spends half its time on those questions.
+            auto activate = [&](auto& v, const auto& u) {
+                if (KIND != LIN_FWD) return;
+                if (DUAL) lin_act_all<LACT_SWIGLU>(v, u);
+                else if (a.act == LACT_RELU) lin_act_all<LACT_RELU>(v, v);
+                else if (a.act == LACT_SILU) lin_act_all<LACT_SILU>(v, v);
+                else if (a.act == LACT_GELU) lin_act_all<LACT_GELU>(v, v);
+            };
+            auto values = [&](const float (&acc)[16], float (&v)[NV]) {
+                float u[NV];
+                if constexpr (DUAL) {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const float got = __shfl_xor_sync(0xFFFFFFFFu, h ? acc[2 * i] : acc[2 * i + 1], 16);
+                        v[i] = (h ? got : acc[2 * i]) + b0;
+                        u[i] = (h ? acc[2 * i + 1] : got) + b1;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) v[i] = KIND == LIN_FWD ? acc[i] + b0 : acc[i];
+                }
+                activate(v, u);
+            };
+            auto quick16 = [&](auto indexed, int ab) {
+                constexpr bool IDX = decltype(indexed)::value;
+                uint16_t* d = static_cast<uint16_t*>(out_of(t, a.out[WG ? t.which : 0])) + (c & ~1);
+                const int first = h + RS * odd;             // this lane's first row of a unit
+                if (!IDX) d += static_cast<long long>(t.r0 + uh * 16 + first) * a.ldo;
+                const long long step = 2 * RS * a.ldo;
+                int left = c < a.C ? t.nrows - uh * 16 - first : 0;
+                const bool bf16 = a.out_type == LIN_BF16;
+                int orow = IDX ? rows_of(t, uh * 16, 16) : 0;
+                take(ab);
+                uint32_t r[16];
+                const uint32_t at = tmem + lane_addr + ab * BN;
+                if (uh < units) tmem_ld16_start(at + uh * 16, r);
+#pragma unroll 1
+                for (int un = uh; un < units; un += 2, left -= 32) {
+                    float acc[16], v[NV];
+                    tmem_ld16_wait(r);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) acc[k] = __uint_as_float(r[k]);
+                    if (un + 2 < units) tmem_ld16_start(at + un * 16 + 32, r);
+                    const int now = orow;
+                    if (IDX && un + 2 < units) orow = rows_of(t, un * 16 + 32, 16);
+                    values(acc, v);
+                    uint32_t x[NV / 2];
+                    if (bf16) {
+#pragma unroll
+                        for (int i = 0; i < NV / 2; ++i) x[i] = lin_pack_bf16(v[2 * i], v[2 * i + 1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NV / 2; ++i) x[i] = lin_pack_f16(v[2 * i], v[2 * i + 1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NV / 2; ++i)
+                        x[i] = __byte_perm(x[i], __shfl_xor_sync(0xFFFFFFFFu, x[i], 1), pick);
+                    if constexpr (IDX) {
+#pragma unroll
+                        for (int i = 0; i < NV / 2; ++i) {
+                            const int o = __shfl_sync(0xFFFFFFFFu, now, first + 2 * RS * i);
+                            if (o >= 0 && 2 * RS * i < left)
+                                *reinterpret_cast<uint32_t*>(d + static_cast<long long>(o) * a.ldo) = x[i];
+                        }
+                    } else {
+                        uint16_t* q = d;
+#pragma unroll
+                        for (int i = 0; i < NV / 2; ++i, q += step)
+                            if (2 * RS * i < left) *reinterpret_cast<uint32_t*>(q) = x[i];
+                        d += 32 * a.ldo;
+                    }
+                }
+                release(ab);
+            };
+            // 16 rows of unit un into a fp32 output
+            auto quick32 = [&](auto indexed, int un, const float (&acc)[16]) {
+                constexpr bool IDX = decltype(indexed)::value;
+                float v[NV];
+                const int orow = IDX ? rows_of(t, un * 16, 16) : 0;
+                values(acc, v);
+                float* d = static_cast<float*>(out_of(t, a.out[WG ? t.which : 0])) + c;
+                const int left = c < a.C ? t.nrows - un * 16 - h : 0;
+                if constexpr (IDX) {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int o = __shfl_sync(0xFFFFFFFFu, orow, h + RS * i);
+                        if (o >= 0 && RS * i < left) d[static_cast<long long>(o) * a.ldo] = v[i];
+                    }
+                } else {
+                    d += static_cast<long long>(t.r0 + un * 16 + h) * a.ldo;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i, d += RS * a.ldo)
+                        if (RS * i < left) *d = v[i];
+                }
+            };
+            const bool quick = split == 1 && !a.z[0] && !res_all && (SPANS || pair_out);
+            using Yes = std::integral_constant<bool, true>;
+            using No = std::integral_constant<bool, false>;
             if (split > 1 && parts > 0 &&
                 !lt_poll<16>(red_empty, (parts - 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
                 latch_error(a.err, ERR_ETIMEOUT, parts, KID_LINEAR);
@@ -729,7 +830,11 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[k] = 0.0f;
                 });
-            } else if (!SPANS || nkb <= kLtPromote) {
+            } else if (!SPANS && quick) {
+                if (!WG && a.scatter) quick16(Yes{}, acc & 1);
+                else quick16(No{}, acc & 1);
+                ++acc;
+            } else if (!SPANS || (nkb <= kLtPromote && !quick)) {
                 const int ab = acc & 1;
                 bool ready = false;
                 uint32_t r[16];
@@ -769,6 +874,16 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     }
                     release(ab);
                 }
+                if (quick) {
+                    const bool idx = !WG && a.scatter;
+#pragma unroll
+                    for (int i = 0; i < NU; ++i) {
+                        if (uh + 2 * i < units) {
+                            if (idx) quick32(Yes{}, uh + 2 * i, v[i]);
+                            else quick32(No{}, uh + 2 * i, v[i]);
+                        }
+                    }
+                } else
                 units_do([&](int, float (&x)[16]) {   // the units in turn through v[0]: one copy of the code above
 #pragma unroll
                     for (int k = 0; k < 16; ++k) x[k] = v[0][k];
