@@ -3,7 +3,7 @@
 // rows of each group, taken before the rounding.
 //
 // Bound by memory: dy, z (z_up) read once, dz (dz_up) written once.  A CTA owns
-// 64 columns and a strip of rows, each thread VEC = 8 consecutive columns (one
+// some columns and a strip of rows, each thread VEC = 8 consecutive columns (one
 // 16-byte access per row; VEC = 1 when a base or row stride is not 16-byte
 // aligned).  Column sums stay in the thread's fp32 registers, meet in shared
 // memory in a fixed order and, when a group's rows are split over the CTAs of a
@@ -33,13 +33,21 @@ struct LinGradArgs {
     int* err;
 };
 
-constexpr int kLgCols = 64, kLgThreads = 256;
+constexpr int kLgThreads = 256;
+// Columns of a CTA: 64 where column sums are wanted (many CTAs over the rows' strips), else 256 (fewer, longer rows).
+constexpr int kLgSumCols = 64, kLgWideCols = 256;
 
-template <int VEC>
-__device__ __forceinline__ void lg_load(const void* p, size_t at, int type, float v[VEC]) {
+template <int TYPE>
+__device__ __forceinline__ float lg_float(uint16_t v) {
+    return TYPE == LIN_BF16 ? bf16_to_f32(v) : __half2float(__ushort_as_half(v));
+}
+
+// VEC values of the 16-bit type TYPE, or of fp32.
+template <int VEC, int TYPE>
+__device__ __forceinline__ void lg_load(const void* p, size_t at, bool f32, float v[VEC]) {
     if constexpr (VEC == 1) {
-        v[0] = lin_load(p, at, type);
-    } else if (type == LIN_F32) {
+        v[0] = f32 ? static_cast<const float*>(p)[at] : lg_float<TYPE>(static_cast<const uint16_t*>(p)[at]);
+    } else if (f32) {
         const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i) {
@@ -51,41 +59,40 @@ __device__ __forceinline__ void lg_load(const void* p, size_t at, int type, floa
         const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
         for (int i = 0; i < VEC / 2; ++i) {
-            const uint16_t lo = w[i] & 0xFFFF, hi = w[i] >> 16;
-            v[2 * i] = type == LIN_BF16 ? bf16_to_f32(lo) : __half2float(__ushort_as_half(lo));
-            v[2 * i + 1] = type == LIN_BF16 ? bf16_to_f32(hi) : __half2float(__ushort_as_half(hi));
+            v[2 * i] = lg_float<TYPE>(w[i] & 0xFFFF);
+            v[2 * i + 1] = lg_float<TYPE>(w[i] >> 16);
         }
     }
 }
 
-template <int VEC>
-__device__ __forceinline__ void lg_store(void* p, size_t at, int type, const float v[VEC]) {
+template <int VEC, int TYPE>
+__device__ __forceinline__ void lg_store(void* p, size_t at, const float v[VEC]) {
     uint16_t* d = static_cast<uint16_t*>(p) + at;
     if constexpr (VEC == 1) {
-        d[0] = lin_cvt16(v[0], type);
+        d[0] = lin_cvt16(v[0], TYPE);
     } else {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < VEC / 2; ++i)
-            w[i] = static_cast<uint32_t>(lin_cvt16(v[2 * i], type)) |
-                   (static_cast<uint32_t>(lin_cvt16(v[2 * i + 1], type)) << 16);
+            w[i] = TYPE == LIN_BF16 ? lin_pack_bf16(v[2 * i], v[2 * i + 1]) : lin_pack_f16(v[2 * i], v[2 * i + 1]);
         *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
 // grid (column blocks, row strips, groups); with db the strips of a group form one cluster.  Without db and without
 // packing the rows of all groups are strips of one.
-template <int VEC, bool UP>
-__global__ void __launch_bounds__(kLgThreads) lin_grad_kernel(const LinGradArgs a) {
+template <int VEC, bool UP, int TYPE, int COLS>
+__global__ void __launch_bounds__(kLgThreads, 4) lin_grad_kernel(LinGradArgs a) {
     namespace cg = cooperative_groups;
-    constexpr int TX = kLgCols / VEC, TY = kLgThreads / TX;
+    constexpr int TX = COLS / VEC, TY = kLgThreads / TX;
     __shared__ float part[UP ? 2 : 1][kLgThreads * VEC];   // [row lane][column]
-    __shared__ float sums[UP ? 2 : 1][kLgCols];
+    __shared__ float sums[UP ? 2 : 1][COLS];
     pdl_wait();
     pdl_trigger();
     const int e = blockIdx.z, tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-    const int c = blockIdx.x * kLgCols + tx * VEC;
+    const int c = blockIdx.x * COLS + tx * VEC;
     const bool on = c < a.N;   // VEC divides N on the vector path
+    const bool f32 = a.dy_type == LIN_F32;
     const bool want_db = a.db[0] != nullptr || a.db[1] != nullptr;
     int p0, p1;
     bool ok = true;
@@ -107,8 +114,8 @@ __global__ void __launch_bounds__(kLgThreads) lin_grad_kernel(const LinGradArgs 
         for (int i = 0; i < VEC; ++i) zero[i] = 0.0f;
         for (int r = p1 - p0 + ty; r < end; r += TY) {
             const size_t gi = static_cast<size_t>(g0 + p0 + r) * a.lddz + c;
-            lg_store<VEC>(a.dz[0], gi, a.type, zero);
-            if (UP) lg_store<VEC>(a.dz[1], gi, a.type, zero);
+            lg_store<VEC, TYPE>(a.dz[0], gi, zero);
+            if (UP) lg_store<VEC, TYPE>(a.dz[1], gi, zero);
         }
     }
     float s0[VEC], s1[UP ? VEC : 1];
@@ -117,67 +124,55 @@ __global__ void __launch_bounds__(kLgThreads) lin_grad_kernel(const LinGradArgs 
         s0[i] = 0.0f;
         if (UP) s1[i] = 0.0f;
     }
-    constexpr int U = VEC == 1 ? 4 : 2;   // rows whose loads are in flight together
-    for (int r0 = r_lo + ty; r0 < r_hi; r0 += U * TY) {
-        float dy[U][VEC], z[U][VEC], u[UP ? U : 1][VEC];
+#pragma unroll 1   // (more rows in flight a thread cost more threads than they gain: 44 us, two rows 83 us, four 105 us)
+    for (int r = r_lo + ty; r < r_hi; r += TY) {
+        const int src = lin_index(a.dy_rows, a.dy_total, r, a.err);
+        if (!on) continue;
+        float dy[VEC], z[VEC], g[VEC];
+        const size_t zi = static_cast<size_t>(r) * a.ldz + c, gi = static_cast<size_t>(g0 + r) * a.lddz + c;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int r = r0 + k * TY;
-            const int src = r < r_hi ? lin_index(a.dy_rows, a.dy_total, r, a.err) : -1;
-            const size_t zi = static_cast<size_t>(r) * a.ldz + c;
+        for (int i = 0; i < VEC; ++i) dy[i] = z[i] = 0.0f;
+        if (src >= 0) lg_load<VEC, TYPE>(a.dy, static_cast<size_t>(src) * a.lddy + c, f32, dy);
+        if (a.act != LACT_NONE) lg_load<VEC, TYPE>(a.z[0], zi, false, z);
+        if constexpr (UP) {
+            float u[VEC];
+            lg_load<VEC, TYPE>(a.z[1], zi, false, u);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) dy[k][i] = z[k][i] = 0.0f;
-            if (on && src >= 0) lg_load<VEC>(a.dy, static_cast<size_t>(src) * a.lddy + c, a.dy_type, dy[k]);
-            if (on && r < r_hi && a.act != LACT_NONE) lg_load<VEC>(a.z[0], zi, a.type, z[k]);
-            if (UP) {
-                if (on && r < r_hi) lg_load<VEC>(a.z[1], zi, a.type, u[UP ? k : 0]);
+            for (int i = 0; i < VEC; ++i) {
+                const float sg = lin_sigmoid(z[i]);
+                g[i] = dy[i] * u[i] * (sg * (1.0f + z[i] * (1.0f - sg)));
+                u[i] = dy[i] * (z[i] * sg);
+                s0[i] += g[i];
+                s1[i] += u[i];
+            }
+            if (a.dz[1]) lg_store<VEC, TYPE>(a.dz[1], gi, u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                g[i] = a.act == LACT_NONE ? dy[i] : dy[i] * lin_slope(a.act, z[i]);
+                s0[i] += g[i];
             }
         }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int r = r0 + k * TY;
-            if (!on || r >= r_hi) continue;
-            const size_t gi = static_cast<size_t>(g0 + r) * a.lddz + c;
-            float g[VEC];
-            if (UP) {
-                float gu[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float sg = 1.0f / (1.0f + expf(-z[k][i]));
-                    gu[i] = dy[k][i] * (z[k][i] * sg);
-                    g[i] = dy[k][i] * u[UP ? k : 0][i] * (sg * (1.0f + z[k][i] * (1.0f - sg)));
-                    s0[i] += g[i];
-                    s1[UP ? i : 0] += gu[i];
-                }
-                if (a.dz[1]) lg_store<VEC>(a.dz[1], gi, a.type, gu);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    g[i] = a.act == LACT_NONE ? dy[k][i] : dy[k][i] * lin_slope(a.act, z[k][i]);
-                    s0[i] += g[i];
-                }
-            }
-            if (a.dz[0]) lg_store<VEC>(a.dz[0], gi, a.type, g);
-        }
+        if (a.dz[0]) lg_store<VEC, TYPE>(a.dz[0], gi, g);
     }
     if (!want_db) return;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        part[0][ty * kLgCols + tx * VEC + i] = s0[i];
-        if constexpr (UP) part[1][ty * kLgCols + tx * VEC + i] = s1[i];
+        part[0][ty * COLS + tx * VEC + i] = s0[i];
+        if constexpr (UP) part[1][ty * COLS + tx * VEC + i] = s1[i];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < (UP ? 2 : 1) * kLgCols; i += kLgThreads) {
-        const int w = i / kLgCols, col = i % kLgCols;
+    for (int i = threadIdx.x; i < (UP ? 2 : 1) * COLS; i += kLgThreads) {
+        const int w = i / COLS, col = i % COLS;
         float t = 0.0f;
-        for (int y = 0; y < TY; ++y) t += part[w][y * kLgCols + col];
+        for (int y = 0; y < TY; ++y) t += part[w][y * COLS + col];
         sums[w][col] = t;
     }
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
     if (cl.block_rank() == 0 && ok) {
-        for (int i = threadIdx.x; i < (UP ? 2 : 1) * kLgCols; i += kLgThreads) {
-            const int w = i / kLgCols, col = i % kLgCols, cc = blockIdx.x * kLgCols + col;
+        for (int i = threadIdx.x; i < (UP ? 2 : 1) * COLS; i += kLgThreads) {
+            const int w = i / COLS, col = i % COLS, cc = blockIdx.x * COLS + col;
             float t = 0.0f;
             for (unsigned k = 0; k < cl.num_blocks(); ++k) t += *cl.map_shared_rank(&sums[w][col], k);
             if (cc < a.N && a.db[w]) {

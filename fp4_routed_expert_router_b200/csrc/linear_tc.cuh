@@ -58,11 +58,13 @@ constexpr int kLtM = 128;            // TMEM lanes of a CTA: A rows of its tile
 constexpr int kLtBK = 64;            // terms per stage: one 128-byte swizzle row
 constexpr int kLtATile = kLtM * 128; // bytes of one A tile of a stage
 constexpr int kLtEpiWarps = 8;
+constexpr int kLtThreads = (4 + kLtEpiWarps) * 32;
 constexpr int kLtMaxStages = 12;
 constexpr int kLtPromote = 10;       // fp32 outputs: stages summed in the tensor core before the sum moves to registers
-constexpr int kLtRaster = 8;         // row tiles walked together, so that operands of neighbouring tiles meet in L2
+constexpr int kLtRaster = 8;         // row tiles walked together
+constexpr int kLtRegs = 168;         // registers a thread starts with
+static_assert(128 * 56 + 256 * 224 == kLtThreads * kLtRegs);
 constexpr int kLtOffPrefix = 256;     // shared memory: barriers, then tile prefix, first rows and counts of the groups
-constexpr int kLtThreads = (4 + kLtEpiWarps) * 32;
 
 struct LtPlan {
     int bn;         // output rows of a tile
@@ -249,7 +251,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* red_full = acc_empty + 2;                    // every part of a split tile is in shared memory
     uint64_t* red_empty = red_full + 1;                    // and has been read
-    int* tprefix = reinterpret_cast<int*>(smem + kLtOffPrefix);   // [E+1] tiles before group e (forward, dgrad)
+    int* tprefix = reinterpret_cast<int*>(smem + kLtOffPrefix);   // [E+1] row tiles before group e (forward, dgrad)
     int* gstart = tprefix + a.E + 1;                              // [E] first row of group e
     int* gcount = gstart + a.E;                                   // [E] its rows, -1: not a sound group
     // split: the parts of this CTA's items (four rows x 32 lanes), [round * warps + warp][rank][4][32]
@@ -286,14 +288,14 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
         }
     }
     pdl_wait();
-    if (warp == 0) {   // the groups, and the tiles before each
+    if (warp == 0) {   // the groups, and the row tiles before each
         int work = 0;
         for (int base = 0; base < a.E; base += 32) {
             const int e = base + lane;
             int p0 = 0, p1 = 0;
             bool ok = true;
             if (e < a.E) ok = lin_group(a.offsets, a.rows, e, a.err, &p0, &p1);
-            const int mine = (p1 - p0 + BN - 1) / BN * p.n_ct;
+            const int mine = (p1 - p0 + BN - 1) / BN;
             int incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -317,12 +319,15 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     pdl_trigger();
     const uint32_t tmem = tmem_base_s;
     const int n_rt_w = WG ? (a.out_n + BN - 1) / BN : 0;
-    const int n_work = WG ? p.n_ct * n_rt_w * a.E * (a.b[1] ? 2 : 1) : tprefix[a.E];
+    const int n_work = WG ? p.n_ct * n_rt_w * a.E * (a.b[1] ? 2 : 1) : tprefix[a.E] * p.n_ct;
     const int w0 = blockIdx.x / csize, G = gridDim.x / csize;
+    const int half_kb = (a.Q + kLtBK - 1) / kLtBK;   // dgrad: stages of the first pair
 
-    // Tile w of the walk; false when its group is not sound (nothing is computed or written).
+    // Tile w of the walk; false when its group is not sound (nothing is computed or written).  Row tiles (of all groups,
+    // one after the other) are taken eight at a time, all their c tiles before the next: neighbours share operands
+    // in L2, and groups with many rows, bound by the MMAs, run beside groups with few, bound by reading weights.
     auto tile_of = [&](int w, LtTile& t) -> bool {
-        int v, n_rt, nkb;
+        int v = w, n_rt, nkb;
         t.which = 0;
         if (WG) {
             const int per = p.n_ct * n_rt_w;
@@ -331,31 +336,32 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             t.e = ve % a.E;
             t.which = ve / a.E;
             n_rt = n_rt_w;
-            t.p0 = a.packed ? lin_packed(gstart[t.e], t.e) : gstart[t.e];
-            t.nq = gcount[t.e];
-            if (t.nq < 0) return false;
-            nkb = (t.nq + kLtBK - 1) / kLtBK;
         } else {
-            int lo = 0, hi = a.E - 1;   // the last group that starts at or before w (empty groups start where they end)
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (tprefix[mid] <= w) lo = mid; else hi = mid - 1;
-            }
-            t.e = lo;
-            v = w - tprefix[lo];
-            n_rt = (tprefix[lo + 1] - tprefix[lo]) / p.n_ct;
-            t.nq = a.Q;
-            nkb = (a.Q + kLtBK - 1) / kLtBK * (KIND == LIN_DGRAD && a.b[1] ? 2 : 1);
+            n_rt = tprefix[a.E];
         }
         const int blk = v / (kLtRaster * p.n_ct);
         v -= blk * kLtRaster * p.n_ct;
         const int in_blk = min(kLtRaster, n_rt - blk * kLtRaster);
-        t.c0 = (v / in_blk * cg + (cg == 2 ? rank : 0)) * p.ct;
-        const int rt = blk * kLtRaster + v % in_blk;
+        const int ct = v / in_blk;
+        int rt = blk * kLtRaster + v - ct * in_blk;
+        t.c0 = (ct * cg + (cg == 2 ? rank : 0)) * p.ct;
         if (WG) {
+            t.p0 = a.packed ? lin_packed(gstart[t.e], t.e) : gstart[t.e];
+            t.nq = gcount[t.e];
+            if (t.nq < 0) return false;
+            nkb = (t.nq + kLtBK - 1) / kLtBK;
             t.r0 = rt * BN;
             t.nrows = min(BN, a.out_n - t.r0);
         } else {
+            int lo = 0, hi = a.E - 1;   // the last group that starts at or before rt (empty groups start where they end)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (tprefix[mid] <= rt) lo = mid; else hi = mid - 1;
+            }
+            t.e = lo;
+            rt -= tprefix[lo];
+            t.nq = a.Q;
+            nkb = half_kb * (KIND == LIN_DGRAD && a.b[1] ? 2 : 1);
             t.r0 = gstart[t.e] + rt * BN;
             t.p0 = a.packed ? lin_packed(gstart[t.e], t.e) + rt * BN : t.r0;
             t.nrows = min(BN, gcount[t.e] - rt * BN);
@@ -374,13 +380,14 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     };
     auto stage_a = [&](int st) { return smem + p.off_ring + static_cast<size_t>(st) * p.stage_bytes; };
     auto stage_b = [&](int st) { return stage_a(st) + kLtATile; };
-    const int half_kb = (a.Q + kLtBK - 1) / kLtBK;   // dgrad: stages of the first pair
     const uint32_t ring0 = smem_u32(smem + p.off_ring);
     const bool epilogue = warp >= 4;
-    // The epilogue of the span kernels holds a tile's sums in registers: 128 a thread on top of its work.  384 threads
-    // start with 168 each; 128 x 56 + 256 x 224 is the same number.
+    // The epilogue needs more registers than the other warps: a tile's sums in the span kernels (128 a thread), a unit's
+    // values and the next one's residual elsewhere (spilled, those loads were waited for on the spot: 270 us instead of
+    // 190 at 8,192 x 5,120 with an fp32 residual).  384 threads start with 168 each (checked when a context is created);
+    // 128 x 56 + 256 x 224 is the same number.
     if (!epilogue) {
-    if constexpr (SPANS) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lt_elect()) {
@@ -488,7 +495,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     }
     } else {
         // ------------------------------------------------------------ epilogue
-        if constexpr (SPANS) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // A block of NR rows: this lane has NR values of one c; for SwiGLU gate and up of every other row of one c.
         const int uh = (warp - 4) >> 2;
         const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -723,17 +730,10 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     else send(un, v);
                 }
             };
-            // The short way for the common outputs (no residual, no z, 16-bit in pairs or fp32): what a value's way out
-            // depends on is known here at compile time.  The general way spends half its time on those questions.
-            auto activate = [&](auto& v, const auto& u) {
-                if (KIND != LIN_FWD) return;
-                if (DUAL) lin_act_all<LACT_SWIGLU>(v, u);
-                else if (a.act == LACT_RELU) lin_act_all<LACT_RELU>(v, v);
-                else if (a.act == LACT_SILU) lin_act_all<LACT_SILU>(v, v);
-                else if (a.act == LACT_GELU) lin_act_all<LACT_GELU>(v, v);
-            };
-            auto values = [&](const float (&acc)[16], float (&v)[NV]) {
-                float u[NV];
+            // The short way for the common outputs: 16-bit in pairs with or without z, index and residual, and plain fp32.
+            // What a value's way out depends on is known here at compile time; the general way above spends half its
+            // time on those questions.
+            auto preact = [&](const float (&acc)[16], float (&v)[NV], float (&u)[NV]) {
                 if constexpr (DUAL) {
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
@@ -745,42 +745,118 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
 #pragma unroll
                     for (int i = 0; i < NV; ++i) v[i] = KIND == LIN_FWD ? acc[i] + b0 : acc[i];
                 }
-                activate(v, u);
             };
-            auto quick16 = [&](auto indexed, int ab) {
+            auto activate = [&](float (&v)[NV], const float (&u)[NV]) {
+                if (KIND != LIN_FWD) return;
+                if (DUAL) lin_act_all<LACT_SWIGLU>(v, u);
+                else if (a.act == LACT_RELU) lin_act_all<LACT_RELU>(v, v);
+                else if (a.act == LACT_SILU) lin_act_all<LACT_SILU>(v, v);
+                else if (a.act == LACT_GELU) lin_act_all<LACT_GELU>(v, v);
+            };
+            // this lane's pairs: (c, c + 1) of rows first + 2 RS i of the unit
+            const int first = h + RS * odd;
+            auto pack = [&](const float (&v)[NV], bool bf16, uint32_t (&x)[NV / 2]) {
+                if (bf16) {
+#pragma unroll
+                    for (int i = 0; i < NV / 2; ++i) x[i] = lin_pack_bf16(v[2 * i], v[2 * i + 1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NV / 2; ++i) x[i] = lin_pack_f16(v[2 * i], v[2 * i + 1]);
+                }
+#pragma unroll
+                for (int i = 0; i < NV / 2; ++i)
+                    x[i] = __byte_perm(x[i], __shfl_xor_sync(0xFFFFFFFFu, x[i], 1), pick);
+            };
+            auto put = [&](uint16_t* q, long long step, int left, const uint32_t (&x)[NV / 2]) {
+#pragma unroll
+                for (int i = 0; i < NV / 2; ++i, q += step)
+                    if (2 * RS * i < left) *reinterpret_cast<uint32_t*>(q) = x[i];
+            };
+            auto quick16 = [&](auto indexed, auto with_residual, int ab) {
                 constexpr bool IDX = decltype(indexed)::value;
+                constexpr int RES = decltype(with_residual)::value;   // 0 none, 1 fp32, 2 16-bit pairs
+                constexpr int NR = RES == 1 ? NV : NV / 2;
                 uint16_t* d = static_cast<uint16_t*>(out_of(t, a.out[WG ? t.which : 0])) + (c & ~1);
-                const int first = h + RS * odd;             // this lane's first row of a unit
-                if (!IDX) d += static_cast<long long>(t.r0 + uh * 16 + first) * a.ldo;
-                const long long step = 2 * RS * a.ldo;
+                const long long row = t.r0 + uh * 16 + first;
+                if (!IDX) d += row * a.ldo;
+                uint16_t* z0 = static_cast<uint16_t*>(a.z[0]) + row * a.ldz + (c & ~1);
+                const long long z1 = DUAL ? static_cast<uint16_t*>(a.z[1]) - static_cast<uint16_t*>(a.z[0]) : 0;
                 int left = c < a.C ? t.nrows - uh * 16 - first : 0;
-                const bool bf16 = a.out_type == LIN_BF16;
+                const bool bf16 = a.out_type == LIN_BF16, zbf16 = a.type == LIN_BF16, rbf16 = res_type == LIN_BF16;
                 int orow = IDX ? rows_of(t, uh * 16, 16) : 0;
+                // the residual of a unit, as it lies there
+                uint32_t rn[RES ? NR : 1];
+                auto fetch = [&](int un, int idx, int left) {
+                    const void* base = WG ? out_of(t, a.out[t.which]) : a.res;
+                    if constexpr (RES == 1) {
+                        const float* q = static_cast<const float*>(base) + c;
+                        if (!IDX) q += static_cast<long long>(t.r0 + un * 16 + h) * ldr;
+                        const int l1 = c < a.C ? t.nrows - un * 16 - h : 0;
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) {
+                            const int o = IDX ? __shfl_sync(0xFFFFFFFFu, idx, h + RS * i) : 0;
+                            rn[i] = 0u;
+                            if (RS * i < l1 && o >= 0)
+                                rn[i] = __float_as_uint(q[IDX ? static_cast<long long>(o) * ldr : RS * i * ldr]);
+                        }
+                    } else if constexpr (RES == 2) {
+                        const uint16_t* q = static_cast<const uint16_t*>(base) + (c & ~1);
+                        if (!IDX) q += static_cast<long long>(t.r0 + un * 16 + first) * ldr;
+#pragma unroll
+                        for (int i = 0; i < NV / 2; ++i) {
+                            const int o = IDX ? __shfl_sync(0xFFFFFFFFu, idx, first + 2 * RS * i) : 0;
+                            rn[i] = 0u;
+                            if (2 * RS * i < left && o >= 0)
+                                rn[i] = *reinterpret_cast<const uint32_t*>(
+                                    q + (IDX ? static_cast<long long>(o) * ldr : 2 * RS * i * ldr));
+                        }
+                    }
+                };
+                if (RES && uh < units) fetch(uh, orow, left);
                 take(ab);
                 uint32_t r[16];
                 const uint32_t at = tmem + lane_addr + ab * BN;
                 if (uh < units) tmem_ld16_start(at + uh * 16, r);
 #pragma unroll 1
                 for (int un = uh; un < units; un += 2, left -= 32) {
-                    float acc[16], v[NV];
+                    float acc[16], v[NV], u[NV];
                     tmem_ld16_wait(r);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) acc[k] = __uint_as_float(r[k]);
-                    if (un + 2 < units) tmem_ld16_start(at + un * 16 + 32, r);
+                    if (un + 2 < units) tmem_ld16_start(at + un * 16 + 32, r);   // lands while this unit is finished
                     const int now = orow;
                     if (IDX && un + 2 < units) orow = rows_of(t, un * 16 + 32, 16);
-                    values(acc, v);
-                    uint32_t x[NV / 2];
-                    if (bf16) {
+                    uint32_t rv[RES ? NR : 1];
+                    if constexpr (RES != 0) {
 #pragma unroll
-                        for (int i = 0; i < NV / 2; ++i) x[i] = lin_pack_bf16(v[2 * i], v[2 * i + 1]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < NV / 2; ++i) x[i] = lin_pack_f16(v[2 * i], v[2 * i + 1]);
+                        for (int i = 0; i < NR; ++i) rv[i] = rn[i];
+                        __syncwarp();   // (the residual may be the output: a neighbour writes this lane's value)
+                        if (un + 2 < units) fetch(un + 2, orow, left - 32);
                     }
+                    preact(acc, v, u);
+                    uint32_t x[NV / 2];
+                    if (KIND == LIN_FWD && a.z[0]) {
+                        pack(v, zbf16, x);
+                        put(z0, 2 * RS * a.ldz, left, x);
+                        if (DUAL && a.z[1]) {
+                            pack(u, zbf16, x);
+                            put(z0 + z1, 2 * RS * a.ldz, left, x);
+                        }
+                        z0 += 32 * a.ldz;
+                    }
+                    activate(v, u);
+                    if constexpr (RES == 1) {
 #pragma unroll
-                    for (int i = 0; i < NV / 2; ++i)
-                        x[i] = __byte_perm(x[i], __shfl_xor_sync(0xFFFFFFFFu, x[i], 1), pick);
+                        for (int i = 0; i < NV; ++i) v[i] += __uint_as_float(rv[i]);
+                    } else if constexpr (RES == 2) {
+#pragma unroll
+                        for (int i = 0; i < NV / 2; ++i) {
+                            const uint32_t w = __byte_perm(rv[i], __shfl_xor_sync(0xFFFFFFFFu, rv[i], 1), pick);
+                            v[2 * i] += rbf16 ? bf16_to_f32(w & 0xFFFF) : __half2float(__ushort_as_half(w & 0xFFFF));
+                            v[2 * i + 1] += rbf16 ? bf16_to_f32(w >> 16) : __half2float(__ushort_as_half(w >> 16));
+                        }
+                    }
+                    pack(v, bf16, x);
                     if constexpr (IDX) {
 #pragma unroll
                         for (int i = 0; i < NV / 2; ++i) {
@@ -789,10 +865,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                                 *reinterpret_cast<uint32_t*>(d + static_cast<long long>(o) * a.ldo) = x[i];
                         }
                     } else {
-                        uint16_t* q = d;
-#pragma unroll
-                        for (int i = 0; i < NV / 2; ++i, q += step)
-                            if (2 * RS * i < left) *reinterpret_cast<uint32_t*>(q) = x[i];
+                        put(d, 2 * RS * a.ldo, left, x);
                         d += 32 * a.ldo;
                     }
                 }
@@ -801,9 +874,10 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             // 16 rows of unit un into a fp32 output
             auto quick32 = [&](auto indexed, int un, const float (&acc)[16]) {
                 constexpr bool IDX = decltype(indexed)::value;
-                float v[NV];
+                float v[NV], u[NV];
                 const int orow = IDX ? rows_of(t, un * 16, 16) : 0;
-                values(acc, v);
+                preact(acc, v, u);
+                activate(v, u);
                 float* d = static_cast<float*>(out_of(t, a.out[WG ? t.which : 0])) + c;
                 const int left = c < a.C ? t.nrows - un * 16 - h : 0;
                 if constexpr (IDX) {
@@ -819,7 +893,13 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                         if (RS * i < left) *d = v[i];
                 }
             };
-            const bool quick = split == 1 && !a.z[0] && !res_all && (SPANS || pair_out);
+            // An fp32 residual without an activation in between is where a span kernel's sums start: its loads run
+            // beside the products.
+            const bool start = SPANS && !DUAL && split == 1 && res_all && res_type == LIN_F32 &&
+                               (KIND != LIN_FWD || a.act == LACT_NONE) && !a.z[0];
+            const bool quick = split == 1 && (SPANS ? !a.z[0] && (!res_all || start)
+                                                    : pair_out && (!a.z[0] || pair_z) &&
+                                                          (!res_all || res_type == LIN_F32 || pair_res));
             using Yes = std::integral_constant<bool, true>;
             using No = std::integral_constant<bool, false>;
             if (split > 1 && parts > 0 &&
@@ -831,8 +911,18 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     for (int k = 0; k < 16; ++k) v[k] = 0.0f;
                 });
             } else if (!SPANS && quick) {
-                if (!WG && a.scatter) quick16(Yes{}, acc & 1);
-                else quick16(No{}, acc & 1);
+                const bool idx = !WG && a.scatter;
+                const int res = !res_all ? 0 : res_type == LIN_F32 ? 1 : 2;
+                if (KIND == LIN_FWD && res == 1) {
+                    if (idx) quick16(Yes{}, std::integral_constant<int, 1>{}, acc & 1);
+                    else quick16(No{}, std::integral_constant<int, 1>{}, acc & 1);
+                } else if (KIND != LIN_DGRAD && res == 2) {
+                    if (idx) quick16(Yes{}, std::integral_constant<int, 2>{}, acc & 1);
+                    else quick16(No{}, std::integral_constant<int, 2>{}, acc & 1);
+                } else {
+                    if (idx) quick16(Yes{}, std::integral_constant<int, 0>{}, acc & 1);
+                    else quick16(No{}, std::integral_constant<int, 0>{}, acc & 1);
+                }
                 ++acc;
             } else if (!SPANS || (nkb <= kLtPromote && !quick)) {
                 const int ab = acc & 1;
@@ -856,10 +946,26 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             } else if constexpr (SPANS) {   // spans summed in registers
                 constexpr int NU = 8;   // units of this warp
                 float v[NU][16];
+                if (!start) {
 #pragma unroll
-                for (int i = 0; i < NU; ++i)
+                    for (int i = 0; i < NU; ++i)
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[i][k] = 0.0f;
+                        for (int k = 0; k < 16; ++k) v[i][k] = 0.0f;
+                } else {
+                    const bool idx = !WG && a.scatter;
+                    const float* q = static_cast<const float*>(WG ? out_of(t, a.out[t.which]) : a.res) + c;
+#pragma unroll
+                    for (int i = 0; i < NU; ++i) {
+                        const int un = uh + 2 * i;
+                        const int orow = idx ? rows_of(t, un * 16, 16) : 0, left = c < a.C ? t.nrows - un * 16 : 0;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int o = idx ? __shfl_sync(0xFFFFFFFFu, orow, k) : t.r0 + un * 16 + k;
+                            v[i][k] = 0.0f;
+                            if (k < left && o >= 0) v[i][k] = q[static_cast<long long>(o) * ldr];
+                        }
+                    }
+                }
                 for (int k0 = 0; k0 < nkb; k0 += kLtPromote, ++acc) {
                     const int ab = acc & 1;
                     take(ab);
@@ -878,9 +984,10 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     const bool idx = !WG && a.scatter;
 #pragma unroll
                     for (int i = 0; i < NU; ++i) {
-                        if (uh + 2 * i < units) {
-                            if (idx) quick32(Yes{}, uh + 2 * i, v[i]);
-                            else quick32(No{}, uh + 2 * i, v[i]);
+                        const int un = uh + 2 * i;
+                        if (un < units) {
+                            if (idx) quick32(Yes{}, un, v[i]);
+                            else quick32(No{}, un, v[i]);
                         }
                     }
                 } else
@@ -1015,8 +1122,9 @@ inline double lt_shape(const LinArgs& a, int cg, int split, int bn, const int* s
     if (stage < (dual ? 560 : 480)) stage = dual ? 560 : 480;
     const double rounds = a.E == 1 || wg ? static_cast<double>((static_cast<long long>(tiles) + slots - 1) / slots)
                                          : (tiles / slots > 1 ? tiles / slots + 0.5 : 1.0);
-    const double tile = nkb / split * stage, out = 12.0 * bn * fill;   // out: the epilogue, hidden but for the last
-    return rounds * (tile > out ? tile : out) + out / (split > 1 ? 2 : 1) + (split > 1 ? 3000 + 100 * split : 0) +
+    // out: a tile's epilogue (3,600 cycles at 256 rows), hidden but for the last; and what finding a tile takes
+    const double tile = nkb / split * stage, out = 14.0 * bn * fill;
+    return rounds * ((tile > out ? tile : out) + 900) + out / (split > 1 ? 2 : 1) + (split > 1 ? 3000 + 100 * split : 0) +
            (cg > 1 ? 500 : 0);
 }
 
@@ -1114,9 +1222,13 @@ cudaError_t lt_allow(int bytes) {
                        reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, 2, false>),
                        reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, 1, true>),
                        reinterpret_cast<const void*>(lin_tc_kernel<KIND, DUAL, 2, true>)};
-    for (const void* f : k) {
-        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    for (int i = 0; i < 4; ++i) {
+        cudaError_t e = cudaFuncSetAttribute(k[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        cudaFuncAttributes at;
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k[i]);
         if (e != cudaSuccess) return e;
+        // the split of registers between the warps adds up to what a block starts with only at this many a thread
+        if (at.numRegs != kLtRegs) return cudaErrorInvalidKernelImage;
     }
     return cudaSuccess;
 }

@@ -1038,22 +1038,34 @@ cudaError_t lin_pack(moe_fp4_ctx* c, const LinCopies& k, void* scratch, const in
                     dim3(kLpThreads), 0, s, a);
 }
 
+template <int COLS>
+void (*lin_grad_pick(bool vec, bool up, bool bf16))(LinGradArgs) {
+    if (vec)
+        return up ? (bf16 ? lin_grad_kernel<8, true, LIN_BF16, COLS> : lin_grad_kernel<8, true, LIN_F16, COLS>)
+                  : (bf16 ? lin_grad_kernel<8, false, LIN_BF16, COLS> : lin_grad_kernel<8, false, LIN_F16, COLS>);
+    return up ? (bf16 ? lin_grad_kernel<1, true, LIN_BF16, COLS> : lin_grad_kernel<1, true, LIN_F16, COLS>)
+              : (bf16 ? lin_grad_kernel<1, false, LIN_BF16, COLS> : lin_grad_kernel<1, false, LIN_F16, COLS>);
+}
+
 cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
     const bool db = g.db[0] || g.db[1], by_group = db || g.packed;
-    // Strips of rows.  With db those of a group form a cluster (8 CTAs at most) and should hold enough rows for the
-    // meeting of their sums to be small beside the loads; else 64 rows a strip keep every SM loading.
+    const bool wide = !db && g.N >= kLgWideCols;
+    const int cols = wide ? kLgWideCols : kLgSumCols, col_blocks = (g.N + cols - 1) / cols;
     const int per_group = by_group ? (g.rows + g.E - 1) / g.E : g.rows;
-    int strips = db ? per_group / 128 : (per_group + 63) / 64;
-    const int most = db ? 8 : 65535;
-    strips = strips < 1 ? 1 : strips > most ? most : strips;
     auto vec_ok = [](const void* p, long long ld, int type) {
         const uintptr_t step = type == LIN_F32 ? 4 : 8;
         return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % step == 0;
     };
     bool vec = g.N % 8 == 0 && vec_ok(g.dy, g.lddy, g.dy_type) && vec_ok(g.dz[0], g.lddz, g.type) &&
                vec_ok(g.dz[1], g.lddz, g.type) && vec_ok(g.z[0], g.ldz, g.type) && vec_ok(g.z[1], g.ldz, g.type);
+    // Strips of rows.  With db those of a group form a cluster (8 CTAs at most) and should hold enough rows for the
+    // meeting of their sums to be small beside the loads.  Else 64 rows (8,192 x 2,304 SwiGLU: 42 us; 47 with 350) or,
+    // as groups differ in size, 32 of an average group (12,288 rows in 64 groups: 73 us; 177 in one strip a group).
+    int strips = db ? per_group / (vec ? 128 : 32) : (per_group + 63) / (by_group ? 32 : 64);
+    const int most = db ? 8 : 65535;
+    strips = strips < 1 ? 1 : strips > most ? most : strips;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((g.N + kLgCols - 1) / kLgCols), static_cast<unsigned>(strips),
+    cfg.gridDim = dim3(static_cast<unsigned>(col_blocks), static_cast<unsigned>(strips),
                        static_cast<unsigned>(by_group ? g.E : 1));
     cfg.blockDim = dim3(kLgThreads);
     cfg.stream = s;
@@ -1073,11 +1085,10 @@ cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
         eb = take_event(c);
         cudaEventRecord(ea, s);
     }
-    const bool up = g.act == LACT_SWIGLU;
-    cudaError_t e = up ? (vec ? cudaLaunchKernelEx(&cfg, lin_grad_kernel<8, true>, g)
-                              : cudaLaunchKernelEx(&cfg, lin_grad_kernel<1, true>, g))
-                       : (vec ? cudaLaunchKernelEx(&cfg, lin_grad_kernel<8, false>, g)
-                              : cudaLaunchKernelEx(&cfg, lin_grad_kernel<1, false>, g));
+    const bool up = g.act == LACT_SWIGLU, bf16 = g.type == LIN_BF16;
+    void (*const kernel)(LinGradArgs) =
+        wide ? lin_grad_pick<kLgWideCols>(vec, up, bf16) : lin_grad_pick<kLgSumCols>(vec, up, bf16);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, g);
     if (prof) {
         cudaEventRecord(eb, s);
         c->prof.push_back({"linear_dz", ea, eb});
