@@ -74,6 +74,7 @@ struct LtPlan {
     int bbox;       // rows of one K-major B box
     int stages, stage_bytes, off_ring, off_red, smem;
     int n_ct;       // tiles along c
+    int paired;     // SwiGLU forward: both weights in one map (1: w first in memory, 2: w_up)
     int tmem_cols;
     int grid;       // CTAs
 };
@@ -202,6 +203,27 @@ __device__ __forceinline__ void lt_tma3(uint32_t dst, const CUtensorMap* map, in
             : "memory");
 }
 
+// SwiGLU's interleaved A tile in one copy: 64 values of 16 rows of both weights, four times (lt_encode_pair).
+template <int CG>
+__device__ __forceinline__ void lt_tma5(uint32_t dst, const CUtensorMap* map, int c0, int c3, int c4, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(0), "r"(c3), "r"(c4), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(0), "r"(c3), "r"(c4), "r"(bar)
+            : "memory");
+}
+
+__device__ __forceinline__ void lt_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // One lane of a converged warp.  The compiler then knows that a single thread issues TMA and MMA instructions; behind
 // a plain lane test it serialises each of them over the warp (75 cycles apiece, measured).
 __device__ __forceinline__ bool lt_elect() {
@@ -286,6 +308,10 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                          "r"(static_cast<uint32_t>(p.tmem_cols)));
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         }
+    }
+    if (tid == 0) {
+        lt_prefetch_map(&maps.a0);
+        lt_prefetch_map(&maps.b0);
     }
     pdl_wait();
     if (warp == 0) {   // the groups, and the row tiles before each
@@ -413,7 +439,9 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     const uint32_t bar = bar0 + ring.st * 8;
                     if (cg == 1 || rank == 0) mbar_arrive_expect_tx(&full[ring.st], all);   // both CTAs' bytes
                     if (KIND == LIN_FWD) {
-                        if (DUAL) {
+                        if (DUAL && p.paired) {
+                            lt_tma5<CG>(sa, &maps.a0, kb * kLtBK, t.c0 / 16, t.e, bar);
+                        } else if (DUAL) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 lt_tma3<CG>(sa + i * 4096, &maps.a0, kb * kLtBK, t.c0 + 16 * i, t.e, bar);
@@ -619,8 +647,9 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
         // c of this lane in lane group lg, and the bias there
         auto col = [&](const LtTile& t, int lg) { return t.c0 + (DUAL ? 16 * lg + (lane & 15) : 32 * lg + lane); };
         auto bias_of = [&](const LtTile& t, int m, int c) {
-            return KIND == LIN_FWD && a.bias[m] && c < a.C
-                       ? lin_load(a.bias[m], static_cast<size_t>(t.e) * a.C + c, a.bias_type) : 0.0f;
+            const void* b = a.bias[DUAL && p.paired == 2 ? 1 - m : m];
+            return KIND == LIN_FWD && b && c < a.C ? lin_load(b, static_cast<size_t>(t.e) * a.C + c, a.bias_type)
+                                                   : 0.0f;
         };
         // Output rows of NR rows from row `first` of the tile, when they are indexed: lane i has row i's.
         auto rows_of = [&](const LtTile& t, int first, int nr) {
@@ -643,8 +672,9 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     const float got = __shfl_xor_sync(0xFFFFFFFFu, h ? acc[2 * i] : acc[2 * i + 1], 16);
-                    v[i] = (h ? got : acc[2 * i]) + b0;
-                    u[i] = (h ? acc[2 * i + 1] : got) + b1;
+                    const float lo = (h ? got : acc[2 * i]) + b0, up = (h ? acc[2 * i + 1] : got) + b1;
+                    v[i] = p.paired == 2 ? up : lo;
+                    u[i] = p.paired == 2 ? lo : up;
                 }
             } else {
 #pragma unroll
@@ -740,6 +770,14 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                         const float got = __shfl_xor_sync(0xFFFFFFFFu, h ? acc[2 * i] : acc[2 * i + 1], 16);
                         v[i] = (h ? got : acc[2 * i]) + b0;
                         u[i] = (h ? acc[2 * i + 1] : got) + b1;
+                    }
+                    if (p.paired == 2) {   // lanes 0-15 hold w_up's rows (b0 and b1 are swapped too)
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) {
+                            const float x = v[i];
+                            v[i] = u[i];
+                            u[i] = x;
+                        }
                     }
                 } else {
 #pragma unroll
@@ -1042,19 +1080,24 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
 }
 
 // ------------------------------------------------------------------ host side
-// Tensor map of boxes of 64 x `rows` 16-bit values of a stack of matrices, 128-byte swizzle, innermost dimension
-// contiguous; strides in elements.
-inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
-                      uint64_t s2, uint32_t rows) {
-    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-    if (!encode) {
+inline PFN_cuTensorMapEncodeTiled_v12000 lt_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
         cudaDriverEntryPointQueryResult q;
         void* f = nullptr;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
             q != cudaDriverEntryPointSuccess)
-            return false;
-        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }
+            return nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return encode;
+}
+
+// Tensor map of boxes of 64 x `rows` 16-bit values of a stack of matrices, 128-byte swizzle, innermost dimension
+// contiguous; strides in elements.
+inline bool lt_encode(CUtensorMap* map, int type, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+                      uint64_t s2, uint32_t rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = lt_encoder();
+    if (!encode) return false;
     const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1 * 2, s2 * 2};
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(kLtBK), rows, 1}, es[3] = {1, 1, 1};
     return encode(map, type == LIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
@@ -1069,6 +1112,8 @@ inline bool lt_tma_ok(const void* p, long long ld, long long gstride) {
            gstride < (1LL << 38);
 }
 
+inline int lt_pairable(const LinArgs& a);
+
 // One candidate tile shape and what it is estimated to take, in SM cycles.
 inline double lt_shape(const LinArgs& a, int cg, int split, int bn, const int* slots_of, int smem_limit,
                        LtPlan* p) {
@@ -1079,8 +1124,9 @@ inline double lt_shape(const LinArgs& a, int cg, int split, int bn, const int* s
     p->split = split;
     p->ct = dual ? kLtM / 2 : kLtM;
     p->n_ct = (a.C + p->ct * cg - 1) / (p->ct * cg);
+    p->paired = lt_pairable(a);
     const int brows = bn / cg;
-    p->bbox = brows < 64 ? brows : 64;
+    p->bbox = brows < 64 || a.E == 1 ? brows : 64;   // groups end anywhere: small boxes load little behind them
     p->stage_bytes = kLtATile + ((wg ? (brows + 63) / 64 * 64 : brows) * 128 + 1023) / 1024 * 1024;
     p->off_ring = (kLtOffPrefix + 4 * (3 * a.E + 1) + 1023) / 1024 * 1024;
     // items: bn / 4 quarters x 4 lane groups, in rounds of all the cluster's warps
@@ -1119,7 +1165,7 @@ inline double lt_shape(const LinArgs& a, int cg, int split, int bn, const int* s
     const double bytes = kLtATile + brows * 128 * fill;
     double stage = 2.0 * bn * fill;
     if (stage < bytes / 48) stage = bytes / 48;
-    if (stage < (dual ? 560 : 480)) stage = dual ? 560 : 480;
+    if (stage < 480) stage = 480;
     const double rounds = a.E == 1 || wg ? static_cast<double>((static_cast<long long>(tiles) + slots - 1) / slots)
                                          : (tiles / slots > 1 ? tiles / slots + 0.5 : 1.0);
     // out: a tile's epilogue (3,600 cycles at 256 rows), hidden but for the last; and what finding a tile takes
@@ -1148,6 +1194,32 @@ inline LtPlan lt_plan(const LinArgs& a, const int* slots, int smem_limit) {
     return best;
 }
 
+// Both weights of SwiGLU as one five-dimensional tensor (K, 16 rows, the two weights, blocks of 16 rows, groups), whose
+// boxes are the interleaved A tile: possible where whole blocks of 16 rows lie in memory and the weights' distance is a
+// stride that a map can hold.
+inline int lt_pairable(const LinArgs& a) {
+    if (a.kind != LIN_FWD || !a.a[1] || a.C % 16) return 0;
+    const intptr_t d = reinterpret_cast<intptr_t>(a.a[1]) - reinterpret_cast<intptr_t>(a.a[0]);
+    const intptr_t far = static_cast<intptr_t>(1) << 39;
+    return d > 0 && d < far ? 1 : d < 0 && -d < far ? 2 : 0;
+}
+
+inline bool lt_encode_pair(CUtensorMap* map, const LinArgs& a, int paired) {
+    const intptr_t d = reinterpret_cast<intptr_t>(a.a[1]) - reinterpret_cast<intptr_t>(a.a[0]);
+    const cuuint64_t lda = static_cast<cuuint64_t>(a.lda) * 2;
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(a.Q), 16, 2, static_cast<cuuint64_t>(a.C / 16),
+                                static_cast<cuuint64_t>(a.E)};
+    const cuuint64_t strides[4] = {lda, static_cast<cuuint64_t>(d < 0 ? -d : d), lda * 16,
+                                   a.E > 1 ? static_cast<cuuint64_t>(a.a_gstride) * 2 : lda * a.C};
+    const cuuint32_t box[5] = {kLtBK, 16, 2, 4, 1}, es[5] = {1, 1, 1, 1, 1};
+    PFN_cuTensorMapEncodeTiled_v12000 encode = lt_encoder();
+    return encode && encode(map,
+                            a.type == LIN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+                            const_cast<void*>(a.a[paired == 1 ? 0 : 1]), dims, strides, box, es,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     const uint64_t C = a.C, Q = a.Q, E = a.E, lda = a.lda, ldb = a.ldb;
     const uint64_t R = static_cast<uint64_t>(a.b_rows > 0 ? a.b_rows : 1);   // rows of B (wgrad: of both)
@@ -1163,11 +1235,12 @@ inline bool lt_maps(const LinArgs& a, const LtPlan& p, LtMaps* m) {
     const uint64_t inner = fwd ? Q : C, outer = fwd ? C : Q;
     const uint64_t gs = E > 1 ? static_cast<uint64_t>(a.a_gstride) : lda * outer;
     const uint32_t abox = !fwd ? 64 : a.a[1] ? 16 : kLtM;
-    ok = lt_encode(&m->a0, a.type, a.a[0], inner, outer, E, lda, gs, abox) &&
+    ok = (p.paired ? lt_encode_pair(&m->a0, a, p.paired)
+                   : lt_encode(&m->a0, a.type, a.a[0], inner, outer, E, lda, gs, abox)) &&
          lt_encode(&m->b0, a.type, a.b[0], Q, R, 1, ldb, ldb * R, p.bbox);
     m->a1 = m->a0;
     m->b1 = m->b0;
-    if (a.a[1]) ok = ok && lt_encode(&m->a1, a.type, a.a[1], inner, outer, E, lda, gs, abox);
+    if (a.a[1] && !p.paired) ok = ok && lt_encode(&m->a1, a.type, a.a[1], inner, outer, E, lda, gs, abox);
     if (a.b[1]) ok = ok && lt_encode(&m->b1, a.type, a.b[1], Q, R, 1, ldb, ldb * R, p.bbox);
     return ok;
 }

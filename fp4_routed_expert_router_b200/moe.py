@@ -467,18 +467,22 @@ class Context:
         def call(s, other, y):
             z = z_up = None
             if y is None:
-                y = torch.empty((y_total, N), dtype=out_dtype or _PLAIN[x.dtype], device=x.device)
-            elif out_dtype is not None and out_dtype != y.dtype:
-                chk.fail("y and out_dtype differ")
-            py, ldy = chk.matrix(y, "y", y_total, N)
+                if out_dtype is not None and out_dtype not in _TYPES:
+                    chk.fail(f"out_dtype is {out_dtype}")
+                y = x.new_empty((y_total, N), dtype=out_dtype or _PLAIN[x.dtype])
+                py, ldy = y.data_ptr(), N
+            else:
+                if out_dtype is not None and out_dtype != y.dtype:
+                    chk.fail("y and out_dtype differ")
+                py, ldy = chk.matrix(y, "y", y_total, N)
             if save:
-                z = torch.empty((R, N), dtype=_PLAIN[x.dtype], device=x.device)
+                z = x.new_empty((R, N), dtype=_PLAIN[x.dtype])
                 z_up = torch.empty_like(z) if w_up is not None else None
             a = LinearArgs(R, K, N, wdt, act_id, 0 if offsets is None else E,
                            None if offsets is None else offsets.data_ptr(), pxr, pyr, x_total, y_total, px, pw, pu,
                            ldx, ldw, gs, pb, pbu, bt, rt, pr, ldr, py, ldy, _TYPES[y.dtype], 0,
                            None if z is None else z.data_ptr(), None if z_up is None else z_up.data_ptr(), N)
-            scratch = chk.scratch(a, self.lib.moe_fp4_linear_scratch, x.device)
+            scratch = chk.scratch(a, self.lib.moe_fp4_linear_scratch, x)
             if other is not None:
                 chk.keep(other, x, w, w_up, offsets, bias, bias_up, residual, x_rows, y_rows, y, z, z_up, scratch)
             rc = self.lib.moe_fp4_linear(self.h, ctypes.byref(a), s)
@@ -568,31 +572,40 @@ class Context:
         t16 = _PLAIN[x.dtype]
 
         def call(s, other, dx, dw, dw_up, db, db_up):
-            def new(shape, dtype):
-                return torch.empty(shape, dtype=dtype, device=x.device)
-
             pdx = pdw = pdwu = pdb = pdbu = None
             lddx = lddw = dgs = dxt = dwt = 0
             if need_dx:
-                dx = new((dx_total, K), t16) if dx is None else dx
-                pdx, lddx = chk.matrix(dx, "dx", dx_total, K)
+                if dx is None:
+                    dx = x.new_empty((dx_total, K), dtype=t16)
+                    pdx, lddx = dx.data_ptr(), K
+                else:
+                    pdx, lddx = chk.matrix(dx, "dx", dx_total, K)
                 dxt = _TYPES[dx.dtype]
             if need_dw:
+                shape = lead + (K,)
                 if dw is None:
-                    dw = new(lead + (K,), dw_dtype or (t16 if dw_up is None else dw_up.dtype))
-                pdw, lddw, dgs = chk.layout(dw, "dw", lead + (K,))
+                    dtype = dw_dtype or (t16 if dw_up is None else dw_up.dtype)
+                    if dtype not in _TYPES:
+                        chk.fail(f"dw_dtype is {dtype}")
+                    dw = x.new_empty(shape, dtype=dtype)
+                    pdw, lddw, dgs = dw.data_ptr(), K, N * K
+                else:
+                    pdw, lddw, dgs = chk.layout(dw, "dw", shape)
+                    if dw_dtype is not None and dw_dtype != dw.dtype:
+                        chk.fail("dw and dw_dtype differ")
                 dwt = _TYPES[dw.dtype]
-                if dw_dtype is not None and _TYPES.get(dw_dtype) != dwt:
-                    chk.fail("dw and dw_dtype differ")
                 if two:
-                    dw_up = torch.empty_strided(dw.shape, dw.stride(), dtype=dw.dtype, device=x.device) \
-                        if dw_up is None else dw_up
-                    pdwu, ld_up, gs_up = chk.layout(dw_up, "dw_up", lead + (K,))
+                    if dw_up is None:
+                        dw_up = torch.empty_strided(shape, dw.stride(), dtype=dw.dtype, device=dw.device)
+                    pdwu, ld_up, gs_up = chk.layout(dw_up, "dw_up", shape)
                     if _TYPES[dw_up.dtype] != dwt or (ld_up, gs_up) != (lddw, dgs):
                         chk.fail("dw and dw_up differ in type or strides")
             if need_db:
-                db = new(lead, torch.float32) if db is None else db
-                pdb = chk.dense(db, "db", lead, (F32,))
+                if db is None:
+                    db = x.new_empty(lead, dtype=torch.float32)
+                    pdb = db.data_ptr()
+                else:
+                    pdb = chk.dense(db, "db", lead, (F32,))
                 if two:
                     db_up = torch.empty_like(db) if db_up is None else db_up
                     pdbu = chk.dense(db_up, "db_up", lead, (F32,))
@@ -600,7 +613,7 @@ class Context:
                                None if offsets is None else offsets.data_ptr(), pxr, pyr, pdr, x_total, dy_total,
                                dx_total, dyt, pdy, lddy, pz, pzu, ldz, px, pw, pu, ldx, ldw, gs,
                                pdx, lddx, dxt, dwt, pdw, pdwu, lddw, dgs, pdb, pdbu, int(accumulate), 0)
-            scratch = chk.scratch(a, self.lib.moe_fp4_linear_backward_scratch, x.device)
+            scratch = chk.scratch(a, self.lib.moe_fp4_linear_backward_scratch, x)
             if other is not None:
                 chk.keep(other, dy, x, w, w_up, offsets, z, z_up, x_rows, y_rows, dx_rows, dx, dw, dw_up, db, db_up,
                          scratch)
@@ -622,17 +635,18 @@ class _Check:
     def fail(self, why: str):
         raise MoeError(EINVAL, f"{self.what}: {why}")
 
-    def tensor(self, t, name: str, types):
+    def tensor(self, t, name: str, types, shape=None):
+        """Refuse what is no tensor of these types (and this shape) on the context's device."""
         if not isinstance(t, torch.Tensor) or t.get_device() != self.dev:
             self.fail(f"{name} is not a tensor on the context's device {self.dev}")
         if _TYPES.get(t.dtype, -1) not in types:
             self.fail(f"{name} has type {t.dtype}")
+        if shape is not None and t.shape != shape:
+            self.fail(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
     def matrix(self, t, name: str, rows: int, cols: int, types=(BF16, F16, F32)):
         """(address, row stride) of a 2-D tensor with contiguous rows."""
-        self.tensor(t, name, types)
-        if tuple(t.shape) != (rows, cols):
-            self.fail(f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
+        self.tensor(t, name, types, (rows, cols))
         ld, inner = t.stride()
         if inner != 1 and cols > 1:
             self.fail(f"{name} needs a contiguous last dimension")
@@ -644,23 +658,21 @@ class _Check:
 
     def rows(self, x, K: int, wdt: int):
         """(address, row stride, rows) of x."""
-        self.tensor(x, "x", (wdt,))
-        if x.dim() != 2 or x.shape[1] != K:
-            self.fail(f"x has shape {tuple(x.shape)}, not [rows, {K}]")
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            self.fail(f"x is not a tensor of shape [rows, {K}]")
         n = x.shape[0]
-        return *self.matrix(x, "x", n, K, (wdt,)), n
+        at, ld = self.matrix(x, "x", n, K, (wdt,))
+        return at, ld, n
 
     def dense(self, t, name: str, shape, types=(BF16, F16, F32)):
-        self.tensor(t, name, types)
-        if tuple(t.shape) != shape or not t.is_contiguous():
-            self.fail(f"{name} has to be a contiguous tensor of shape {shape}")
+        self.tensor(t, name, types, shape)
+        if not t.is_contiguous():
+            self.fail(f"{name} has to be contiguous")
         return t.data_ptr()
 
     def layout(self, t, name: str, shape, types=(BF16, F16, F32)):
         """(address, row stride, group stride) of [N, K] or [E, N, K] with contiguous rows."""
-        self.tensor(t, name, types)
-        if tuple(t.shape) != tuple(shape):
-            self.fail(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        self.tensor(t, name, types, shape)
         st, n, k = t.stride(), shape[-2], shape[-1]
         ld = st[-2] if n > 1 else k
         gs = st[0] if len(shape) == 3 and shape[0] > 1 else n * ld
@@ -697,7 +709,7 @@ class _Check:
         return t.shape[0]
 
     def index(self, t, name: str, n: int):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or tuple(t.shape) != (n,) or \
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != (n,) or \
                 not t.is_contiguous() or t.get_device() != self.dev:
             self.fail(f"{name} has to be a contiguous int32 [{n}] on the context's device")
         return t.data_ptr()
@@ -717,12 +729,12 @@ class _Check:
                 return call(stream.cuda_stream, stream, *outputs)
 
     @staticmethod
-    def scratch(a, size, device):
+    def scratch(a, size, like):
         """The scratch a call needs, if any, from torch's allocator (so it follows the call's stream)."""
         n = size(ctypes.byref(a))
         if n == 0:
             return None
-        t = torch.empty(n, dtype=torch.uint8, device=device)
+        t = like.new_empty(n, dtype=torch.uint8)
         a.scratch, a.scratch_bytes = t.data_ptr(), n
         return t
 
