@@ -133,13 +133,6 @@ __device__ __forceinline__ uint32_t lt_rank() {
     return r;
 }
 
-// Address of this CTA's shared-memory location in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t lt_map(const void* p, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-    return r;
-}
-
 // Arrive at a barrier anywhere in the cluster.  (Without .release.cluster, which waits for every earlier store of the
 // thread to be visible there; what has to be is ordered by lt_cluster_fence, once per tile.)
 __device__ __forceinline__ void lt_arrive_remote(uint32_t bar) {
@@ -151,10 +144,19 @@ __device__ __forceinline__ void lt_cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Address of this CTA's shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t lt_map(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+
 // Bounded wait for phase `parity` of `bar`.  The probes come without a pause (SLEEP = 0, the two warps whose pace sets the kernel's) or SLEEP ns apart;
-// the timer, whose reading costs about as much as a stage, is looked at every 256 probes only.
+// the timer, whose reading costs about as much as a stage, is looked at every 16 (without pause: 256) probes only.
+// A wait that gives up sets the abort flag of every CTA of the cluster.
 template <int SLEEP>
-__device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
+__device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile int* abort, int csize,
+                                        uint64_t timeout_ns) {
     const uint32_t at = smem_u32(bar);
     uint64_t t0 = 0;
     for (uint32_t n = 1;; ++n) {
@@ -167,13 +169,19 @@ __device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile
             : "r"(at), "r"(parity)
             : "memory");
         if (ok) return true;
+        if (SLEEP && n == 1) t0 = global_timer_ns();   // (these waits have the time)
         if (SLEEP) __nanosleep(SLEEP);
-        if ((n & 255) == 0) {
+        if ((n & (SLEEP ? 15 : 255)) == 0) {
             if (*abort) return false;
             const uint64_t now = global_timer_ns();
             if (t0 == 0) t0 = now;
             if (now - t0 > timeout_ns) {
                 *abort = 1;
+                for (int r = 0; csize > 1 && r < csize; ++r)
+                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                                     lt_map(const_cast<int*>(abort), static_cast<uint32_t>(r))),
+                                 "r"(1)
+                                 : "memory");
                 return false;
             }
         }
@@ -273,6 +281,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* red_full = acc_empty + 2;                    // every part of a split tile is in shared memory
     uint64_t* red_empty = red_full + 1;                    // and has been read
+    uint64_t* all_done = red_empty + 1;                    // the last MMAs
     int* tprefix = reinterpret_cast<int*>(smem + kLtOffPrefix);   // [E+1] row tiles before group e (forward, dgrad)
     int* gstart = tprefix + a.E + 1;                              // [E] first row of group e
     int* gcount = gstart + a.E;                                   // [E] its rows, -1: not a sound group
@@ -294,6 +303,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
         }
         mbar_init(red_full, kLtEpiWarps * split);
         mbar_init(red_empty, kLtEpiWarps * split);
+        mbar_init(all_done, 1);
         abort_s = 0;
     }
     if (warp == 1) {
@@ -430,7 +440,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 const uint32_t all = static_cast<uint32_t>(cg * (kLtATile + nbox * box_b));
                 const int br = (WG ? t.r0 : t.p0) + t.b0;
                 for (int kb = t.kb0; kb < t.kb1; ++kb, ++g, ring.next(S)) {
-                    if (!lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, a.timeout_ns)) {
+                    if (!lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, csize, a.timeout_ns) || *abort_flag) {
                         latch_error(a.err, ERR_ETIMEOUT, g, KID_LINEAR);
                         stop = true;
                         break;
@@ -469,12 +479,12 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     }
                 }
             }
-            if (*abort_flag && (cg == 1 || rank == 0)) {   // copies still in flight land before the CTA may exit
-                volatile int fresh = 0;                    // (a pair's second CTA waits for the first)
-                for (int st = 0; st < S && st < g; ++st) {
+            if (*abort_flag && (cg == 1 || rank == 0)) {   // copies still in flight land before the CTA may exit (a
+                volatile int fresh = 0;                    // pair's second CTA waits for the first); those that a CTA
+                for (int st = 0; st < S && st < g; ++st) { // did not issue any more are given up after 2 ms
                     const int last = st + ((g - 1 - st) / S) * S;
                     fresh = 0;
-                    mbar_wait(&full[st], (last / S) & 1, &fresh);
+                    mbar_wait(&full[st], (last / S) & 1, &fresh, 2000000ull);
                 }
             }
         }
@@ -483,23 +493,30 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
         if (lt_elect()) {
             LtRing ring;
             int acc = 0;
+            bool stop = false;
             const uint64_t ad0 = A_MN ? lt_desc_mn(ring0) : umma_desc_sw128(ring0);
             const uint64_t bd0 = WG ? lt_desc_mn(ring0 + kLtATile) : umma_desc_sw128(ring0 + kLtATile);
-            for (int w = w0; w < n_work; w += G) {
+            for (int w = w0; w < n_work && !stop; w += G) {
                 LtTile t;
                 if (!tile_of(w, t)) continue;
                 const uint32_t idesc = lt_idesc(a.type, A_MN, WG, kLtM * cg, t.n);
                 const int span = SPANS ? kLtPromote : t.kb1 - t.kb0;
                 for (int k0 = t.kb0; k0 < t.kb1; k0 += span, ++acc) {
                     const int ab = acc & 1;
-                    if (!lt_poll<0>(&acc_empty[ab], ((acc >> 1) & 1) ^ 1, abort_flag, a.timeout_ns))
+                    if (!lt_poll<0>(&acc_empty[ab], ((acc >> 1) & 1) ^ 1, abort_flag, csize, a.timeout_ns)) {
                         latch_error(a.err, ERR_ETIMEOUT, acc, KID_LINEAR);
+                        stop = true;
+                        break;
+                    }
                     tc_fence_after();
                     const uint32_t d = tmem + ab * BN;
                     const int k1 = min(t.kb1, k0 + span);
                     for (int kb = k0; kb < k1; ++kb, ring.next(S)) {
-                        if (!lt_poll<0>(&full[ring.st], ring.ph, abort_flag, a.timeout_ns))
+                        if (!lt_poll<0>(&full[ring.st], ring.ph, abort_flag, csize, a.timeout_ns)) {
                             latch_error(a.err, ERR_ETIMEOUT, kb, KID_LINEAR);
+                            stop = true;
+                            break;
+                        }
                         tc_fence_after();
                         const uint64_t off = static_cast<uint64_t>(ring.st * (p.stage_bytes >> 4));
                         int steps = kLtBK / 16;   // the group's last stage may have fewer
@@ -511,14 +528,13 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                                            idesc, kb > k0 || k > 0 ? 1u : 0u);
                         lt_commit<CG>(&empty[ring.st]);
                     }
+                    if (stop) break;
                     lt_commit<CG>(&acc_full[ab]);
                 }
             }
-            for (int k = 1; k <= 2; ++k)   // the last commits land before TMEM is released
-                if (acc >= k) {
-                    volatile int fresh = 0;
-                    mbar_wait(&acc_full[(acc - k) & 1], ((acc - k) >> 1) & 1, &fresh);
-                }
+            lt_commit<CG>(all_done);   // every MMA is done before TMEM is released
+            volatile int fresh = 0;
+            mbar_wait(all_done, 0, &fresh);
         }
     }
     } else {
@@ -699,12 +715,12 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             __syncwarp();   // (the residual may be the output: a neighbour writes this lane's value)
         };
         int acc = 0, parts = 0;
-        for (int w = w0; w < n_work; w += G) {
+        for (int w = w0; w < n_work && !__any_sync(0xFFFFFFFFu, *abort_flag); w += G) {
             LtTile t;
             if (!tile_of(w, t)) continue;
             const int units = (t.nrows + 15) / 16, nkb = t.kb1 - t.kb0;
             auto take = [&](int ab) {
-                if (!lt_poll<32>(&acc_full[ab], (acc >> 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
+                if (!lt_poll<32>(&acc_full[ab], (acc >> 1) & 1, abort_flag, csize, a.timeout_ns) && lane == 0)
                     latch_error(a.err, ERR_ETIMEOUT, acc, KID_LINEAR);
                 tc_fence_after();
             };
@@ -941,7 +957,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             using Yes = std::integral_constant<bool, true>;
             using No = std::integral_constant<bool, false>;
             if (split > 1 && parts > 0 &&
-                !lt_poll<16>(red_empty, (parts - 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
+                !lt_poll<16>(red_empty, (parts - 1) & 1, abort_flag, csize, a.timeout_ns) && lane == 0)
                 latch_error(a.err, ERR_ETIMEOUT, parts, KID_LINEAR);
             if (nkb == 0) {   // an empty group's gradient, or nothing of a short sum
                 units_do([&](int, float (&v)[16]) {
@@ -1042,7 +1058,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 lt_cluster_fence();
                 __syncwarp();
                 if (lane < split) lt_arrive_remote(lt_map(red_full, static_cast<uint32_t>(lane)));
-                if (!lt_poll<16>(red_full, parts & 1, abort_flag, a.timeout_ns) && lane == 0)
+                if (!lt_poll<16>(red_full, parts & 1, abort_flag, csize, a.timeout_ns) && lane == 0)
                     latch_error(a.err, ERR_ETIMEOUT, parts, KID_LINEAR);
                 lt_cluster_fence();
                 const int items = (t.nrows + 3) / 4 * 4;
