@@ -153,10 +153,8 @@ __device__ __forceinline__ uint32_t lt_map(const void* p, uint32_t rank) {
 
 // Bounded wait for phase `parity` of `bar`.  The probes come without a pause (SLEEP = 0, the two warps whose pace sets the kernel's) or SLEEP ns apart;
 // the timer, whose reading costs about as much as a stage, is looked at every 16 (without pause: 256) probes only.
-// A wait that gives up sets the abort flag of every CTA of the cluster.
 template <int SLEEP>
-__device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile int* abort, int csize,
-                                        uint64_t timeout_ns) {
+__device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
     const uint32_t at = smem_u32(bar);
     uint64_t t0 = 0;
     for (uint32_t n = 1;; ++n) {
@@ -177,11 +175,6 @@ __device__ __forceinline__ bool lt_poll(uint64_t* bar, uint32_t parity, volatile
             if (t0 == 0) t0 = now;
             if (now - t0 > timeout_ns) {
                 *abort = 1;
-                for (int r = 0; csize > 1 && r < csize; ++r)
-                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                                     lt_map(const_cast<int*>(abort), static_cast<uint32_t>(r))),
-                                 "r"(1)
-                                 : "memory");
                 return false;
             }
         }
@@ -440,7 +433,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 const uint32_t all = static_cast<uint32_t>(cg * (kLtATile + nbox * box_b));
                 const int br = (WG ? t.r0 : t.p0) + t.b0;
                 for (int kb = t.kb0; kb < t.kb1; ++kb, ++g, ring.next(S)) {
-                    if (!lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, csize, a.timeout_ns) || *abort_flag) {
+                    if (!lt_poll<0>(&empty[ring.st], ring.ph ^ 1, abort_flag, a.timeout_ns)) {
                         latch_error(a.err, ERR_ETIMEOUT, g, KID_LINEAR);
                         stop = true;
                         break;
@@ -501,9 +494,9 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 if (!tile_of(w, t)) continue;
                 const uint32_t idesc = lt_idesc(a.type, A_MN, WG, kLtM * cg, t.n);
                 const int span = SPANS ? kLtPromote : t.kb1 - t.kb0;
-                for (int k0 = t.kb0; k0 < t.kb1; k0 += span, ++acc) {
+                for (int k0 = t.kb0; k0 < t.kb1 && !stop; k0 += span, ++acc) {
                     const int ab = acc & 1;
-                    if (!lt_poll<0>(&acc_empty[ab], ((acc >> 1) & 1) ^ 1, abort_flag, csize, a.timeout_ns)) {
+                    if (!lt_poll<0>(&acc_empty[ab], ((acc >> 1) & 1) ^ 1, abort_flag, a.timeout_ns)) {
                         latch_error(a.err, ERR_ETIMEOUT, acc, KID_LINEAR);
                         stop = true;
                         break;
@@ -512,9 +505,9 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     const uint32_t d = tmem + ab * BN;
                     const int k1 = min(t.kb1, k0 + span);
                     for (int kb = k0; kb < k1; ++kb, ring.next(S)) {
-                        if (!lt_poll<0>(&full[ring.st], ring.ph, abort_flag, csize, a.timeout_ns)) {
+                        if (!lt_poll<0>(&full[ring.st], ring.ph, abort_flag, a.timeout_ns)) {
                             latch_error(a.err, ERR_ETIMEOUT, kb, KID_LINEAR);
-                            stop = true;
+                            stop = true;   // no slot is freed any more: every producer of the pair stops within a ring
                             break;
                         }
                         tc_fence_after();
@@ -528,7 +521,6 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                                            idesc, kb > k0 || k > 0 ? 1u : 0u);
                         lt_commit<CG>(&empty[ring.st]);
                     }
-                    if (stop) break;
                     lt_commit<CG>(&acc_full[ab]);
                 }
             }
@@ -715,12 +707,12 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             __syncwarp();   // (the residual may be the output: a neighbour writes this lane's value)
         };
         int acc = 0, parts = 0;
-        for (int w = w0; w < n_work && !__any_sync(0xFFFFFFFFu, *abort_flag); w += G) {
+        for (int w = w0; w < n_work; w += G) {
             LtTile t;
             if (!tile_of(w, t)) continue;
             const int units = (t.nrows + 15) / 16, nkb = t.kb1 - t.kb0;
             auto take = [&](int ab) {
-                if (!lt_poll<32>(&acc_full[ab], (acc >> 1) & 1, abort_flag, csize, a.timeout_ns) && lane == 0)
+                if (!lt_poll<32>(&acc_full[ab], (acc >> 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
                     latch_error(a.err, ERR_ETIMEOUT, acc, KID_LINEAR);
                 tc_fence_after();
             };
@@ -957,7 +949,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             using Yes = std::integral_constant<bool, true>;
             using No = std::integral_constant<bool, false>;
             if (split > 1 && parts > 0 &&
-                !lt_poll<16>(red_empty, (parts - 1) & 1, abort_flag, csize, a.timeout_ns) && lane == 0)
+                !lt_poll<16>(red_empty, (parts - 1) & 1, abort_flag, a.timeout_ns) && lane == 0)
                 latch_error(a.err, ERR_ETIMEOUT, parts, KID_LINEAR);
             if (nkb == 0) {   // an empty group's gradient, or nothing of a short sum
                 units_do([&](int, float (&v)[16]) {
@@ -1058,7 +1050,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                 lt_cluster_fence();
                 __syncwarp();
                 if (lane < split) lt_arrive_remote(lt_map(red_full, static_cast<uint32_t>(lane)));
-                if (!lt_poll<16>(red_full, parts & 1, abort_flag, csize, a.timeout_ns) && lane == 0)
+                if (!lt_poll<16>(red_full, parts & 1, abort_flag, a.timeout_ns) && lane == 0)
                     latch_error(a.err, ERR_ETIMEOUT, parts, KID_LINEAR);
                 lt_cluster_fence();
                 const int items = (t.nrows + 3) / 4 * 4;
