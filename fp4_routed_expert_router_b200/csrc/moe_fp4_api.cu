@@ -903,7 +903,8 @@ bool lin_aligned(const void* p, int type) {
 // Sizes both calls share; what: the call's name in messages.
 moe_fp4_status lin_sizes(moe_fp4_ctx* c, const char* what, int rows, int K, int N, int type, int act, int n_groups,
                          const int32_t* offsets) {
-    if (rows < 0 || K < 1 || N < 1)
+    constexpr int most = 1 << 30;   // row and column indices, tiles and packed rows stay in 32 bits
+    if (rows < 0 || K < 1 || N < 1 || rows > most || K > most || N > most)
         return host_fail(c, MOE_FP4_EINVAL, "%s: rows %d / in_features %d / out_features %d", what, rows, K, N);
     if (!lin_type16(type)) return host_fail(c, MOE_FP4_EINVAL, "%s: type %d is not 16-bit", what, type);
     if (act < MOE_FP4_ACT_NONE || act > MOE_FP4_ACT_SWIGLU)

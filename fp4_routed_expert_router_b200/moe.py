@@ -404,8 +404,9 @@ class Context:
         act: "none", "relu", "silu", "gelu" or "swiglu" (silu(x w^T + bias) *
         (x w_up^T + bias_up)).  bias [N], residual [R, N] and y may be of
         either 16-bit type or fp32; y is x's type unless out_dtype or y says
-        otherwise, and residual may be y itself.  Rows may be strided, the last
-        dimension is contiguous.  save: also return z (and z_up, else None), the
+        otherwise, and residual may be y itself (y overlaps no other input).
+        Rows may be strided, the last dimension is contiguous; x or weights
+        whose rows are not 16-byte aligned are copied first.  save: also return z (and z_up, else None), the
         pre-activations that linear_backward takes.  Work runs on ``stream``
         (default: the current one of the context's device)."""
         return self._linear("linear", x, w, None, w_up, bias, bias_up, act, residual, y, out_dtype, save, None, None,
@@ -423,7 +424,8 @@ class Context:
         x_rows (int32 [R]): row i reads x[x_rows[i]], e.g. Routing.perm // k.
         y_rows (int32 [R], distinct): row i goes to y[y_rows[i]] (and takes
         residual[y_rows[i]]), e.g. Routing.perm for rows in entry order.  Rows
-        of y outside every group are left as they were; z is in grouped order."""
+        of y outside every group are left as they were (undefined in a y that
+        this call allocates); z is in grouped order."""
         return self._linear("grouped_linear", x, w, offsets, w_up, bias, bias_up, act, residual, y, out_dtype, save,
                             x_rows, y_rows, stream)
 
@@ -505,7 +507,7 @@ class Context:
         dy [R, N] has x's type or fp32; z (and z_up) are what linear(save=True)
         returned.  dz is rounded to x's type for the products.  dx, dw, dw_up,
         db, db_up may be given as outputs (dx and dw of any of the three
-        types); accumulate adds to the given dw and db instead of overwriting
+        types; none may overlap an input); accumulate adds to the given dw and db instead of overwriting
         them (micro-batches)."""
         return self._linear_backward("linear_backward", dy, x, w, None, w_up, z, z_up, act, need_dx, need_dw, need_db,
                                      dx, dw, dw_up, db, db_up, dw_dtype, accumulate, None, None, None, stream)

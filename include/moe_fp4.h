@@ -405,9 +405,9 @@ enum {
  * means dense.  Strides count elements; the innermost stride is 1.
  */
 typedef struct {
-    int32_t rows;              /* R: rows of the product, >= 0 (grouped rows when n_groups > 0) */
-    int32_t in_features;       /* K >= 1 */
-    int32_t out_features;      /* N >= 1 */
+    int32_t rows;              /* R: rows of the product, 0 .. 2^30 (grouped rows when n_groups > 0) */
+    int32_t in_features;       /* K: 1 .. 2^30 */
+    int32_t out_features;      /* N: 1 .. 2^30 */
     int32_t type;              /* x, w, w_up, z, z_up: MOE_FP4_BF16 or MOE_FP4_F16 */
     int32_t act;               /* MOE_FP4_ACT_* */
     int32_t n_groups;          /* E <= 1024: weights per group; 0: one weight for all rows */
@@ -446,7 +446,8 @@ typedef struct {
  * fp32 and y, z and z_up are rounded once.  With a fp32 y the accumulation is
  * done in fp32 registers over spans of K of at most 640 (the tensor core
  * truncates its fp32 sums, which costs about 1e-9 relative per K); 16-bit
- * outputs do not need that.
+ * outputs do not need that.  A NaN or infinity reaches only the rows (in dw and
+ * db: the groups) whose sums it is part of.
  * Grouped (n_groups > 0): row i of group e takes w[e], bias[e].  Rows of y and
  * z outside every group are left as they were; an empty group does nothing.
  * x_rows and y_rows fuse the gather of token rows into grouped order and the
@@ -458,7 +459,8 @@ typedef struct {
  * (weights only of groups that have rows).  moe_fp4_linear_scratch says how
  * many bytes that takes, from sizes, pointers and strides alone; scratch must
  * stay untouched until the call's work on `stream` is done.  Nothing else is
- * shared, so calls with scratch of their own may overlap in time.
+ * shared, so calls with scratch of their own may overlap in time.  Apart from
+ * residual = y, outputs and scratch must not overlap inputs or one another.
  * Errors: EINVAL, ECUDA; latched: EINVAL (a group that is no part of [0, R] is
  * skipped -- when offsets descend anywhere no result is valid; an x_rows entry
  * outside [0, x_total): that row counts as zero; a y_rows entry outside
@@ -509,6 +511,8 @@ typedef struct {
  * is used as it is), and copies of x and w as in the forward; with groups the
  * rows of dz and x lie there with zeros between the groups, which the sums over
  * rows run into.
+ * Outputs and scratch must not overlap inputs or one another (dx is written
+ * while dy may still be read).
  * Errors: as moe_fp4_linear (a bad y_rows entry counts as a zero dy row).
  */
 size_t moe_fp4_linear_backward_scratch(const moe_fp4_linear_grads *args);

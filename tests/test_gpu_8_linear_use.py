@@ -273,6 +273,21 @@ def test_values_that_are_not_finite_stay_in_their_rows(ctx):
     assert bool(torch.isnan(d1.db[2, 5])) and bool(torch.isnan(d1.dw[2, 5]).all())
 
 
+def test_groups_without_any_row(ctx):
+    """Rows that no group holds, and groups that hold none: y stays, gradients are zero."""
+    g = _gen(55)
+    x, w, dy = _rand(g, 9, 72), _rand(g, 4, 40, 72), _rand(g, 9, 40)
+    od = torch.full((5,), 4, dtype=torch.int32, device="cuda")
+    y = torch.full((9, 40), 2.0, dtype=BF, device="cuda")
+    ctx.grouped_linear(x, w, od, y=y, x_rows=torch.full((9,), -1, dtype=torch.int32, device="cuda"))
+    dw = torch.full_like(w, 3.0, dtype=F)
+    d = ctx.grouped_linear_backward(dy, x, w, od, dx=y.new_full((9, 72), 6.0), need_db=True)
+    ctx.grouped_linear_backward(dy, x, w, od, need_dx=False, dw=dw, accumulate=True)
+    _ok(ctx)
+    assert bool((y == 2).all()) and bool((d.dx == 6).all()) and bool((dw == 3).all())
+    assert bool((d.dw == 0).all()) and bool((d.db == 0).all())
+
+
 def test_bad_indices_in_the_backward_pass(ctx):
     g = _gen(60)
     K, N, R = 72, 40, 30
@@ -311,7 +326,7 @@ def test_the_c_call_refuses(ctx):
             setattr(a, k, v)
         return a
 
-    bad = [dict(rows=-1), dict(in_features=0), dict(out_features=0), dict(type=2), dict(type=7), dict(act=5),
+    bad = [dict(rows=-1), dict(rows=(1 << 30) + 1), dict(in_features=0), dict(out_features=0), dict(type=2), dict(type=7), dict(act=5),
            dict(act=-1), dict(act=4), dict(w_up=w.data_ptr()), dict(n_groups=1025, offsets=x.data_ptr()),
            dict(n_groups=2), dict(offsets=x.data_ptr()), dict(n_groups=-1), dict(x=None), dict(w=None), dict(y=None),
            dict(ldx=63), dict(ldw=-64), dict(ldy=31), dict(y_type=3), dict(bias=x.data_ptr(), bias_type=9),
