@@ -377,9 +377,13 @@ def test_profile_names_the_kernels(ctx):
     assert names == ["linear_pack", "linear", "linear_pack", "linear_dz", "linear_dx", "linear_dw"]
 
 
-@pytest.mark.parametrize("R,K,N", [(2048, 5120, 2304), (16, 5120, 384)])
+@pytest.mark.parametrize("R,K,N", [(2048, 5120, 2304), (16, 81920, 384)])
 def test_wait_limit_runs_out_then_calls_work_again(ctx, R, K, N):
-    """A pair of CTAs and a split sum whose waits give up after a microsecond: ETIMEOUT, and the context goes on."""
+    """A pair of CTAs and a split sum whose waits give up after a microsecond: ETIMEOUT, and the context goes on.
+
+    The epilogue waits for a whole sum and looks at the clock every 1.4 us or so, so the sum has to take many times
+    that: 80 stages of a pair take about 30 us, 160 of each CTA of a split sum (18 KB each at no more than 120 GB/s an
+    SM) at least 24 us.  (A split sum of 5,120 terms is over in 3 us: whether its wait runs out is chance.)"""
     g = _gen(80)
     x, w = _rand(g, R, K), _rand(g, N, K, scale=K ** -0.5)
     good = ctx.linear(x, w)
