@@ -1178,7 +1178,8 @@ inline double lt_shape(const LinArgs& a, int cg, int split, int bn, const int* s
                                          : (tiles / slots > 1 ? tiles / slots + 0.5 : 1.0);
     // out: a tile's epilogue (3,600 cycles at 256 rows), hidden but for the last; and what finding a tile takes
     const double tile = nkb / split * stage, out = 14.0 * bn * fill;
-    return rounds * ((tile > out ? tile : out) + 900) + out / (split > 1 ? 2 : 1) + (split > 1 ? 3000 + 100 * split : 0) +
+    const double both = tile > out ? tile + 0.15 * out : out + 0.15 * tile;   // the hidden part slows the other
+    return rounds * (both + 900) + out / (split > 1 ? 2 : 1) + (split > 1 ? 3000 + 100 * split : 0) +
            (cg > 1 ? 500 : 0);
 }
 
