@@ -1,5 +1,5 @@
 // linear_common.cuh -- what the 16-bit product kernels share: arguments,
-// element conversions, activations and the finishing step of an output value.
+// element conversions, activations, groups and packed rows.
 //
 // Three products per layer, with x [R, K], w [N, K], dz [R, N]:
 //   forward  y[r][n]  = act(sum_k x[r][k] w[n][k] + b[n]) + residual[r][n]
@@ -75,13 +75,8 @@ __device__ __forceinline__ uint32_t lin_pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void lin_store(void* p, size_t i, float v, int type) {
-    if (type == LIN_F32) static_cast<float*>(p)[i] = v;
-    else static_cast<uint16_t*>(p)[i] = lin_cvt16(v, type);
-}
-
-// 1 / (1 + e^-z).  The quotients here and in lin_act are the fast ones (two steps of 2^-24 off, and 0 for divisors above
-// 2^126): far inside the 16-bit rounding that follows, and the fp32 outputs' sums are less exact.
+// 1 / (1 + e^-z).  The quotients here and in lin_act are the fast ones (two steps of 2^-24 off, and 0 for divisors
+// above 2^126): far inside the 16-bit rounding that follows, and the fp32 outputs' sums are less exact.
 __device__ __forceinline__ float lin_sigmoid(float z) { return __fdividef(1.0f, 1.0f + expf(-z)); }
 
 __device__ __forceinline__ float lin_act(int act, float z, float z_up) {

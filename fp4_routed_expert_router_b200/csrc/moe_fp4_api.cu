@@ -1033,9 +1033,10 @@ cudaError_t lin_pack(moe_fp4_ctx* c, const LinCopies& k, void* scratch, const in
     if (k.w) job(w, k.w_at[0], ldw, gs, N, wb);
     if (k.w && w_up) job(w_up, k.w_at[1], ldw, gs, N, wb);
     const long long cols = (lin_padded(K) + kLpCols - 1) / kLpCols;
-    if (blocks > 0x7FFFFFFF || cols > 65535) return cudaErrorInvalidConfiguration;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     return launch_k(c, "linear_pack", lin_pack_kernel,
-                    dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(cols), static_cast<unsigned>(n)),
+                    dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(cols < 65535 ? cols : 65535),
+                         static_cast<unsigned>(n)),
                     dim3(kLpThreads), 0, s, a);
 }
 

@@ -315,6 +315,44 @@ def test_bad_indices_in_the_backward_pass(ctx):
     assert bool((dx[[4, 20]] == 7).all())
 
 
+def test_offsets_that_descend_are_latched(ctx):
+    """No result is valid then, but the call ends, reports it and stays inside its tensors: here every second group is
+    all rows, so that the groups' tiles together are many times what sound groups could have."""
+    g = _gen(61)
+    K, N, R, E, edge = 72, 40, 33, 64, 64
+    x, w, dy = _rand(g, R, K), _rand(g, E, N, K, scale=0.1), _rand(g, R, N)
+    od = torch.tensor([0, R] * (E // 2) + [0], dtype=torch.int32, device="cuda")
+    y, dx = (torch.full((R + 2 * edge, n), 5.0, dtype=BF, device="cuda") for n in (N, K))
+    dw = torch.full((E + 2, N, K), 5.0, dtype=F, device="cuda")
+    ctx.grouped_linear(x, w, od, y=y[edge:-edge])
+    torch.cuda.synchronize()
+    assert ctx.last_error()[0] == moe.EINVAL
+    ctx.grouped_linear_backward(dy, x, w, od, dx=dx[edge:-edge], dw=dw[1:-1], need_db=True)
+    torch.cuda.synchronize()
+    assert ctx.last_error()[0] == moe.EINVAL
+    for t in (y, dx):
+        assert bool((t[:edge] == 5).all()) and bool((t[-edge:] == 5).all())
+    assert bool((dw[0] == 5).all()) and bool((dw[-1] == 5).all())
+    ctx.grouped_linear(x, w[:2], torch.tensor([0, 3, R], dtype=torch.int32, device="cuda"))
+    _ok(ctx)
+
+
+def test_a_row_wider_than_a_grid_of_copies(ctx):
+    """An odd length, which is copied, of more 512-column blocks than a grid's second dimension has.  Whole numbers,
+    whose products and sums are exact in every order."""
+    K = 512 * 65535 + 81
+    g = _gen(62)
+    x, w = (torch.zeros(1, K, dtype=BF, device="cuda") for _ in range(2))
+    at = torch.cat([torch.randint(K, (500,), generator=g, device="cuda"), torch.arange(K - 90, K, device="cuda")])
+    x[0, at] = torch.randint(-8, 9, (590,), generator=g, device="cuda").to(BF)
+    w[0, at] = torch.randint(-8, 9, (590,), generator=g, device="cuda").to(BF)
+    y = ctx.linear(x, w, out_dtype=F)
+    d = ctx.linear_backward(torch.full((1, 1), 3.0, dtype=BF, device="cuda"), x, w)
+    _ok(ctx)
+    assert y.item() == (x.double() * w.double()).sum().item()
+    assert torch.equal(d.dx, 3 * w) and torch.equal(d.dw.to(BF), 3 * x)
+
+
 def test_the_c_call_refuses(ctx):
     x = torch.ones(4, 64, dtype=BF, device="cuda")
     w = torch.ones(32, 64, dtype=BF, device="cuda")
