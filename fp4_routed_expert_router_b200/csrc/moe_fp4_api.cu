@@ -1061,8 +1061,9 @@ cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
     bool vec = g.N % 8 == 0 && vec_ok(g.dy, g.lddy, g.dy_type) && vec_ok(g.dz[0], g.lddz, g.type) &&
                vec_ok(g.dz[1], g.lddz, g.type) && vec_ok(g.z[0], g.ldz, g.type) && vec_ok(g.z[1], g.ldz, g.type);
     // Strips of rows.  With db those of a group form a cluster (8 CTAs at most) and should hold enough rows for the
-    // meeting of their sums to be small beside the loads.  Else 64 rows (8,192 x 2,304 SwiGLU: 42 us; 47 with 350) or,
-    // as groups differ in size, 32 of an average group (12,288 rows in 64 groups: 73 us; 177 in one strip a group).
+    // meeting of their sums to be small beside the loads.  Else 64 rows (8,192 x 2,304 SwiGLU: 37 us; 41 with 16, 40
+    // with 256) or, as groups differ in size, 32 of an average group (12,288 rows in 64 groups, some four times as large
+    // as the average: 65 us; 92 with 64, 184 with 256).
     int strips = db ? per_group / (vec ? 128 : 32) : (per_group + 63) / (by_group ? 32 : 64);
     const int most = db ? 8 : 65535;
     strips = strips < 1 ? 1 : strips > most ? most : strips;
