@@ -52,6 +52,7 @@ struct LinArgs {
     int accumulate;
     void* z[2];
     long long ldz;
+    int late;                 // needs nothing of the kernel launched before it (see lin_tc_kernel)
     int* err;
     unsigned long long timeout_ns;
 };
@@ -98,14 +99,17 @@ __device__ __forceinline__ float lin_slope(int act, float z) {
     return s * (1.0f + z * (1.0f - s));
 }
 
-// Rows [p0, p1) of group e; false (and EINVAL) when they are no part of [0, rows].
+// Rows [p0, p1) of group e; false (and EINVAL) when they are no part of [0, rows].  L2: read past the first-level cache
+// (in linear_pack, whose blocks all wait for it, that would cost 20 us of 40).
+template <bool L2 = false>
 __device__ __forceinline__ bool lin_group(const int32_t* offsets, int rows, int e, int* err, int* p0, int* p1) {
     if (!offsets) {
         *p0 = 0;
         *p1 = rows;
         return true;
     }
-    const int o0 = __ldg(offsets + e), o1 = __ldg(offsets + e + 1);
+    const int o0 = L2 ? __ldcg(offsets + e) : __ldg(offsets + e);
+    const int o1 = L2 ? __ldcg(offsets + e + 1) : __ldg(offsets + e + 1);
     *p0 = o0;
     *p1 = o1;
     if (o0 >= 0 && o0 <= o1 && o1 <= rows) return true;

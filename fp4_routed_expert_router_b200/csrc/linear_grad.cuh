@@ -196,34 +196,35 @@ __global__ void __launch_bounds__(kLgThreads, COLS == kLgSumCols ? 3 : 4) lin_gr
         }
         if (a.dz[0]) lg_store<VEC, TYPE>(a.dz[0], gi, g);
     }
-    if constexpr (!SUMS) return;
-    if (!want_db) return;
+    if constexpr (SUMS) {
+        if (!want_db) return;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        part[0][ty * COLS + tx * VEC + i] = s0[i];
-        if constexpr (UP) part[1][ty * COLS + tx * VEC + i] = s1[i];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < (UP ? 2 : 1) * COLS; i += kLgThreads) {
-        const int w = i / COLS, col = i % COLS;
-        float t = 0.0f;
-        for (int y = 0; y < TY; ++y) t += part[w][y * COLS + col];
-        sums[w][col] = t;
-    }
-    cg::cluster_group cl = cg::this_cluster();
-    cl.sync();
-    if (cl.block_rank() == 0 && ok) {
+        for (int i = 0; i < VEC; ++i) {
+            part[0][ty * COLS + tx * VEC + i] = s0[i];
+            if constexpr (UP) part[1][ty * COLS + tx * VEC + i] = s1[i];
+        }
+        __syncthreads();
         for (int i = threadIdx.x; i < (UP ? 2 : 1) * COLS; i += kLgThreads) {
-            const int w = i / COLS, col = i % COLS, cc = blockIdx.x * COLS + col;
+            const int w = i / COLS, col = i % COLS;
             float t = 0.0f;
-            for (unsigned k = 0; k < cl.num_blocks(); ++k) t += *cl.map_shared_rank(&sums[w][col], k);
-            if (cc < a.N && a.db[w]) {
-                float* d = a.db[w] + static_cast<size_t>(e) * a.N + cc;
-                *d = a.accumulate ? *d + t : t;
+            for (int y = 0; y < TY; ++y) t += part[w][y * COLS + col];
+            sums[w][col] = t;
+        }
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        if (cl.block_rank() == 0 && ok) {
+            for (int i = threadIdx.x; i < (UP ? 2 : 1) * COLS; i += kLgThreads) {
+                const int w = i / COLS, col = i % COLS, cc = blockIdx.x * COLS + col;
+                float t = 0.0f;
+                for (unsigned k = 0; k < cl.num_blocks(); ++k) t += *cl.map_shared_rank(&sums[w][col], k);
+                if (cc < a.N && a.db[w]) {
+                    float* d = a.db[w] + static_cast<size_t>(e) * a.N + cc;
+                    *d = a.accumulate ? *d + t : t;
+                }
             }
         }
+        cl.sync();   // the first CTA has read the others' sums
     }
-    cl.sync();   // the first CTA has read the others' sums
 }
 
 }  // namespace moe

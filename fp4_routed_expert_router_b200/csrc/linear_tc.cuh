@@ -226,6 +226,13 @@ __device__ __forceinline__ void lt_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// A value of the residual, or (L2) of an old dw, which is read past the first-level cache.
+template <bool L2, class T>
+__device__ __forceinline__ T lt_read(const T* p) {
+    if constexpr (L2) return __ldcg(p);
+    else return *p;
+}
+
 // One lane of a converged warp.  The compiler then knows that a single thread issues TMA and MMA instructions; behind
 // a plain lane test it serialises each of them over the warp (75 cycles apiece, measured).
 __device__ __forceinline__ bool lt_elect() {
@@ -317,7 +324,11 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
         lt_prefetch_map(&maps.a0);
         lt_prefetch_map(&maps.b0);
     }
-    pdl_wait();
+    // A backward pass's dw reads nothing that its dx writes, and dx itself has waited for all that came before it: dw
+    // may begin on every SM that dx leaves, and only waits for dx before it ends, so that what follows finds both done.
+    // (What it reads, offsets, operands and the old dw, comes from L2, not from a first-level cache that an earlier
+    // kernel filled.)
+    if (!a.late) pdl_wait();
     if (warp == 0) {   // the groups, and the row tiles before each
         // No sound offsets give more row tiles than this; descending ones, whose groups may overlap, are held to it, so
         // that no count passes 32 bits.
@@ -327,7 +338,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             const int e = base + lane;
             int p0 = 0, p1 = 0;
             bool ok = true;
-            if (e < a.E) ok = lin_group(a.offsets, a.rows, e, a.err, &p0, &p1);
+            if (e < a.E) ok = lin_group<WG>(a.offsets, a.rows, e, a.err, &p0, &p1);
             const int mine = (p1 - p0 + BN - 1) / BN;
             unsigned incl = static_cast<unsigned>(mine);
 #pragma unroll
@@ -625,7 +636,8 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     const int r = RS * (2 * i + odd) + h;
                     const int o = indexed ? __shfl_sync(0xFFFFFFFFu, orow, r) : (r < valid ? row0 + r : -1);
                     raw[i] = 0u;
-                    if (o >= 0 && on) raw[i] = *reinterpret_cast<const uint32_t*>(d + static_cast<long long>(o) * ldr);
+                    if (o >= 0 && on)
+                        raw[i] = lt_read<WG>(reinterpret_cast<const uint32_t*>(d + static_cast<long long>(o) * ldr));
                 }
             } else {
 #pragma unroll
@@ -635,8 +647,8 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                     const long long at = static_cast<long long>(o) * ldr + c;
                     raw[i] = 0u;
                     if (o >= 0 && on)
-                        raw[i] = res_type == LIN_F32 ? static_cast<const uint32_t*>(ptr)[at]
-                                                     : static_cast<const uint16_t*>(ptr)[at];
+                        raw[i] = res_type == LIN_F32 ? lt_read<WG>(static_cast<const uint32_t*>(ptr) + at)
+                                                     : lt_read<WG>(static_cast<const uint16_t*>(ptr) + at);
                 }
             }
         };
@@ -850,7 +862,8 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                             const int o = IDX ? __shfl_sync(0xFFFFFFFFu, idx, h + RS * i) : 0;
                             rn[i] = 0u;
                             if (RS * i < l1 && o >= 0)
-                                rn[i] = __float_as_uint(q[IDX ? static_cast<long long>(o) * ldr : RS * i * ldr]);
+                                rn[i] = __float_as_uint(
+                                    lt_read<WG>(q + (IDX ? static_cast<long long>(o) * ldr : RS * i * ldr)));
                         }
                     } else if constexpr (RES == 2) {
                         const uint16_t* q = static_cast<const uint16_t*>(base) + (c & ~1);
@@ -860,8 +873,8 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                             const int o = IDX ? __shfl_sync(0xFFFFFFFFu, idx, first + 2 * RS * i) : 0;
                             rn[i] = 0u;
                             if (2 * RS * i < left && o >= 0)
-                                rn[i] = *reinterpret_cast<const uint32_t*>(
-                                    q + (IDX ? static_cast<long long>(o) * ldr : 2 * RS * i * ldr));
+                                rn[i] = lt_read<WG>(reinterpret_cast<const uint32_t*>(
+                                    q + (IDX ? static_cast<long long>(o) * ldr : 2 * RS * i * ldr)));
                         }
                     }
                 };
@@ -1015,7 +1028,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
                         for (int k = 0; k < 16; ++k) {
                             const int o = idx ? __shfl_sync(0xFFFFFFFFu, orow, k) : t.r0 + un * 16 + k;
                             v[i][k] = 0.0f;
-                            if (k < left && o >= 0) v[i][k] = q[static_cast<long long>(o) * ldr];
+                            if (k < left && o >= 0) v[i][k] = lt_read<WG>(q + static_cast<long long>(o) * ldr);
                         }
                     }
                 }
@@ -1081,6 +1094,7 @@ lin_tc_kernel(const LinArgs a, const LtPlan p, const __grid_constant__ LtMaps ma
             }
         }
     }
+    if (a.late) pdl_wait();
     tc_fence_before();
     __syncthreads();
     if (csize > 1) lt_cluster_sync();   // no CTA leaves while another may still signal it or read its parts

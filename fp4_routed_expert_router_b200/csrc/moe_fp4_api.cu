@@ -1062,8 +1062,8 @@ cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
                vec_ok(g.dz[1], g.lddz, g.type) && vec_ok(g.z[0], g.ldz, g.type) && vec_ok(g.z[1], g.ldz, g.type);
     // Strips of rows.  With db those of a group form a cluster (8 CTAs at most) and should hold enough rows for the
     // meeting of their sums to be small beside the loads.  Else 64 rows (8,192 x 2,304 SwiGLU: 37 us; 41 with 16, 40
-    // with 256) or, as groups differ in size, 32 of an average group (12,288 rows in 64 groups, some four times as large
-    // as the average: 65 us; 92 with 64, 184 with 256).
+    // with 256) or, as groups differ in size, 32 of an average group (12,288 rows in 64 groups, the largest six times
+    // the average: 65 us; 92 with 64, 184 with 256).
     int strips = db ? per_group / (vec ? 128 : 32) : (per_group + 63) / (by_group ? 32 : 64);
     const int most = db ? 8 : 65535;
     strips = strips < 1 ? 1 : strips > most ? most : strips;
@@ -1330,6 +1330,9 @@ extern "C" moe_fp4_status moe_fp4_linear_backward(moe_fp4_ctx* c, const moe_fp4_
         d.o_gstride = dgs;
         d.out_type = p->dw_type;
         d.accumulate = p->accumulate;
+        // Beginning before dx has ended saves 2 us of 15 where both are short (129 x 256 -> 131; 2,048 x 5,120 -> 384:
+        // 1.5 of 33) and nothing where both fill the GPU for long (8,192 x 5,120 -> 2,304: 535 either way).
+        d.late = want_dx && static_cast<double>(R) * N * K <= 8e9;
         if ((e = lin_run(c, "linear_dw", d, s)) != cudaSuccess) return cuda_fail(c, e, "linear_backward: dw launch");
     }
     return MOE_FP4_OK;

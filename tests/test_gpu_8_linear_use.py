@@ -315,6 +315,42 @@ def test_bad_indices_in_the_backward_pass(ctx):
     assert bool((dx[[4, 20]] == 7).all())
 
 
+@pytest.mark.parametrize("graph", [False, True])
+def test_micro_batches_one_after_the_other(ctx, graph):
+    """Backward calls without a pause, whose kernels begin beside the ends of those before and whose scratch is the
+    same memory each time, give the bits of calls that are waited for."""
+    g = _gen(63)
+    R, K, N, E, n = 70, 136, 72, 3, 12
+    x, w = _rand(g, R, K), _rand(g, E, N, K, scale=0.1)
+    od = torch.tensor([0, 33, 33, R], dtype=torch.int32, device="cuda")
+    z = _rand(g, R, N)
+    dys = [_rand(g, R, N) for _ in range(n)]
+
+    def batches(dw, db, wait):
+        dxs = []
+        for dy in dys:
+            d = ctx.grouped_linear_backward(dy, x, w, od, z=z, act="silu", dw=dw, db=db, need_db=True, accumulate=True)
+            dxs.append(d.dx)
+            if wait:
+                torch.cuda.synchronize()
+        return torch.stack(dxs)
+
+    want_w, want_b = torch.zeros(E, N, K, device="cuda"), torch.zeros(E, N, device="cuda")
+    want_x = batches(want_w, want_b, True)
+    dw, db = torch.zeros_like(want_w), torch.zeros_like(want_b)
+    if graph:
+        rec = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(rec):
+            dx = batches(dw, db, False)
+        dw.zero_()
+        db.zero_()
+        rec.replay()
+    else:
+        dx = batches(dw, db, False)
+    _ok(ctx)
+    assert torch.equal(dx, want_x) and torch.equal(dw, want_w) and torch.equal(db, want_b)
+
+
 def test_offsets_that_descend_are_latched(ctx):
     """No result is valid then, but the call ends, reports it and stays inside its tensors: here every second group is
     all rows, so that the groups' tiles together are many times what sound groups could have."""
