@@ -406,9 +406,10 @@ class Context:
         either 16-bit type or fp32; y is x's type unless out_dtype or y says
         otherwise, and residual may be y itself (y overlaps no other input).
         Rows may be strided, the last dimension is contiguous; x or weights
-        whose rows are not 16-byte aligned are copied first.  save: also return z (and z_up, else None), the
-        pre-activations that linear_backward takes.  Work runs on ``stream``
-        (default: the current one of the context's device)."""
+        whose rows are not 16-byte aligned are copied first.  save: also
+        return z (and z_up, else None), the pre-activations that
+        linear_backward takes.  Work runs on ``stream`` (default: the current
+        one of the context's device)."""
         return self._linear("linear", x, w, None, w_up, bias, bias_up, act, residual, y, out_dtype, save, None, None,
                             stream)
 
@@ -440,9 +441,9 @@ class Context:
         if y_rows is None:
             y_total = R
         elif y is not None:
-            y_total = y.shape[0]
+            y_total = chk.height(y, "y")
         else:
-            y_total = R if residual is None else residual.shape[0]
+            y_total = R if residual is None else chk.height(residual, "residual")
         pw, ldw, gs = chk.layout(w, "w", w.shape)
         pu = None
         if w_up is not None:
@@ -507,8 +508,8 @@ class Context:
         dy [R, N] has x's type or fp32; z (and z_up) are what linear(save=True)
         returned.  dz is rounded to x's type for the products.  dx, dw, dw_up,
         db, db_up may be given as outputs (dx and dw of any of the three
-        types; none may overlap an input); accumulate adds to the given dw and db instead of overwriting
-        them (micro-batches)."""
+        types; none may overlap an input); accumulate adds to the given dw and
+        db instead of overwriting them (micro-batches)."""
         return self._linear_backward("linear_backward", dy, x, w, None, w_up, z, z_up, act, need_dx, need_dw, need_db,
                                      dx, dw, dw_up, db, db_up, dw_dtype, accumulate, None, None, None, stream)
 
@@ -551,8 +552,8 @@ class Context:
         if accumulate and ((need_dw and (dw is None or two and dw_up is None)) or
                            (need_db and (db is None or two and db_up is None))):
             chk.fail("accumulate adds to given outputs")
-        dy_total = R if y_rows is None else dy.shape[0]
-        dx_total = R if dx_rows is None or dx is None else dx.shape[0]
+        dy_total = R if y_rows is None else chk.height(dy, "dy")
+        dx_total = R if dx_rows is None or dx is None else chk.height(dx, "dx")
         pdy, lddy = chk.matrix(dy, "dy", dy_total, N, (wdt, F32))
         dyt = _TYPES[dy.dtype]
         pw, ldw, gs = chk.layout(w, "w", w.shape)
@@ -708,6 +709,11 @@ class _Check:
     def length(self, t, name: str):
         if not isinstance(t, torch.Tensor) or t.dim() != 1:
             self.fail(f"{name} has to be a contiguous int32 vector on the context's device")
+        return t.shape[0]
+
+    def height(self, t, name: str):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            self.fail(f"{name} is not a tensor of two dimensions")
         return t.shape[0]
 
     def index(self, t, name: str, n: int):

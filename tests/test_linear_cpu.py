@@ -167,6 +167,16 @@ def test_grouped_refusals(ctx):
     _refused(lambda: ctx.grouped_linear(x, _x(1, 32, 64).expand(3, 32, 64), od), "overlap")
 
 
+def test_indexed_operands_without_rows_are_refused(ctx):
+    """With an index the number of rows comes from the operand itself, which has to have some."""
+    x, w, od, ix = _x(6, 64), _x(3, 32, 64), torch.zeros(4, dtype=torch.int32), torch.zeros(6, dtype=torch.int32)
+    for bad in (_x(6), torch.zeros(()), 3.0):
+        _refused(lambda: ctx.grouped_linear(x, w, od, y_rows=ix, y=bad), "y is not a tensor")
+        _refused(lambda: ctx.grouped_linear(x, w, od, y_rows=ix, residual=bad), "residual is not a tensor")
+        _refused(lambda: ctx.grouped_linear_backward(bad, x, w, od, y_rows=ix), "dy is not a tensor")
+        _refused(lambda: ctx.grouped_linear_backward(_x(6, 32), x, w, od, dx_rows=ix, dx=bad), "dx is not a tensor")
+
+
 def test_backward_refusals(ctx):
     x, w, dy = _x(4, 64), _x(32, 64), _x(4, 32)
     back = ctx.linear_backward
