@@ -9,8 +9,9 @@ import random
 import pytest
 import torch
 
-from fp4_routed_expert_router_b200 import moe
+from fp4_routed_expert_router_b200 import moe, synth
 from tests import linear_ref as ref
+from tests.gpu_helpers import Filled, check_routing, check_y, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -540,3 +541,58 @@ def test_training_step_of_a_layer_with_routed_and_shared_experts():
             assert _rel(a, t.grad) < tol, name
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("T", [1, 4, 33, 130])
+def test_fp4_layer_with_its_router_and_a_shared_expert(T):
+    """The FP4 layer between this library's own router product and shared expert, without a wait in between and in a
+    replayed graph: the bits of calls that are waited for one by one, the routed part within its bar of the oracle, the
+    shared part of fp64.  There h is rounded to bf16 once (2^-8 of it at most) and sums of its values stay as near in
+    norm; 2 * 2^-8 leaves as much again for the activation and the fp32 sums."""
+    wl = synth.WORKLOADS["tiny"]
+    f = Filled(wl, max_tokens=256, from_host=True)
+    ctx = f.ctx
+    try:
+        H, I, E = wl.hidden, wl.inter, wl.n_experts
+        g = _gen(70 + T)
+        gate, gb = _rand(g, E, H, scale=H ** -0.5), _rand(g, E, dtype=F, scale=0.1)
+        s1, s3, s2 = (_rand(g, *s, scale=s[1] ** -0.5) for s in ((I, H), (I, H), (H, I)))
+        xs = [synth.gen_x(wl.seed, T, H, 5000 + i) for i in range(4)]
+        x = to_dev(xs[0])
+
+        def layer(wait=False):
+            step = torch.cuda.synchronize if wait else (lambda: None)
+            logits = ctx.linear(x, gate, bias=gb, out_dtype=F)
+            step()
+            r, y = ctx.route_forward(0, logits, x)
+            step()
+            h = ctx.linear(x, s1, w_up=s3, act="swiglu")
+            step()
+            return logits, r, y, ctx.linear(h, s2, residual=y, out_dtype=F)
+
+        want = []
+        for v in xs:
+            x.copy_(to_dev(v))
+            logits, r, y, out = layer(wait=True)
+            _ok(ctx)
+            ids, w = check_routing(r, logits.cpu().numpy(), wl.top_k, E)
+            check_y(y.cpu().numpy(), f.oracle_y(0, v, ids, w, range(T)))
+            X = x.view(BF).double()
+            shared = (torch.nn.functional.silu(X @ s1.double().T) * (X @ s3.double().T)) @ s2.double().T
+            assert _rel(out.double() - y.double(), shared) < 2 * 2.0 ** -8
+            want.append((logits.clone(), y.clone(), out.clone()))
+        for v, (a, b, c) in zip(xs, want):
+            x.copy_(to_dev(v))
+            logits, _, y, out = layer()
+            _ok(ctx)
+            assert torch.equal(logits, a) and torch.equal(y, b) and torch.equal(out, c)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            logits, _, y, out = layer()
+        for v, (a, b, c) in zip(xs * 3, want * 3):
+            x.copy_(to_dev(v))
+            graph.replay()
+            assert torch.equal(logits, a) and torch.equal(y, b) and torch.equal(out, c)
+        _ok(ctx)
+    finally:
+        f.close()
