@@ -37,8 +37,11 @@ struct LinGradArgs {
 };
 
 constexpr int kLgThreads = 256;
-// Columns of a CTA: 64 where column sums are wanted (many CTAs over the rows' strips), else 256 (fewer, longer rows).
-constexpr int kLgSumCols = 64, kLgWideCols = 256;
+constexpr int kLgWide = 256;   // columns of a CTA without sums: few CTAs, long rows
+// Columns of a CTA with sums (or of fewer columns than that): a group's strips are 8 at most, so that narrow CTAs are
+// what spreads its rows (7,467 x 108, single columns: 37 us with 32 columns a CTA, 21 with 16; 93 with 64 and a row at
+// a time).
+__host__ __device__ constexpr int lg_cols(int vec, bool sums) { return !sums ? kLgWide : vec == 1 ? 16 : 64; }
 
 template <int TYPE>
 __device__ __forceinline__ float lg_float(uint16_t v) {
@@ -101,15 +104,16 @@ __device__ __forceinline__ void lg_store(void* p, size_t at, const float v[VEC])
     }
 }
 
-// Three CTAs an SM where sums are kept: at four their registers would spill.
 // grid (column blocks, row strips, groups); with db the strips of a group form one cluster.  Without db and without
 // packing the rows of all groups are strips of one.
-template <int VEC, bool UP, int TYPE, int COLS>
-__global__ void __launch_bounds__(kLgThreads, COLS == kLgSumCols ? 3 : 4) lin_grad_kernel(LinGradArgs a) {
+template <int VEC, bool UP, int TYPE, bool SUMS>
+__global__ void __launch_bounds__(kLgThreads, SUMS ? 3 : 4) lin_grad_kernel(LinGradArgs a) {
     namespace cg = cooperative_groups;
-    constexpr int TX = COLS / VEC, TY = kLgThreads / TX;
-    constexpr bool SUMS = COLS == kLgSumCols;   // db may be wanted
-    constexpr bool AHEAD = !SUMS;               // the next row's loads run beside this row's arithmetic
+    constexpr int COLS = lg_cols(VEC, SUMS), TX = COLS / VEC, TY = kLgThreads / TX;
+    constexpr int U = VEC == 1 ? 4 : 1;   // rows a thread loads at a time
+    // A round's loads run beside the arithmetic of the one before, but where their registers are those of the sums
+    // (8,192 x 2,304 SwiGLU with db: 55 us without, 67 with and a CTA less on each SM).
+    constexpr bool AHEAD = VEC == 1 || !SUMS;
     __shared__ float part[UP ? 2 : 1][kLgThreads * VEC];   // [row lane][column]
     __shared__ float sums[UP ? 2 : 1][COLS];
     pdl_wait();
@@ -149,52 +153,67 @@ __global__ void __launch_bounds__(kLgThreads, COLS == kLgSumCols ? 3 : 4) lin_gr
         s0[i] = 0.0f;
         if (UP) s1[i] = 0.0f;
     }
-    LgRaw<VEC> dr = {}, zr = {}, ur = {};
-    auto load = [&](int r, int src) {
-        if (!on || r >= r_hi) return;
-        const size_t zi = static_cast<size_t>(r) * a.ldz + c;
-        dr = LgRaw<VEC>{};
-        if (src >= 0) lg_load<VEC>(a.dy, static_cast<size_t>(src) * a.lddy + c, f32, dr);
-        if (a.act != LACT_NONE) lg_load<VEC>(a.z[0], zi, false, zr);
-        if (UP) lg_load<VEC>(a.z[1], zi, false, ur);
+    LgRaw<VEC> dr[U] = {}, zr[U] = {}, ur[U] = {};
+    int src[U];
+    auto source = [&](int r) {
+#pragma unroll
+        for (int k = 0; k < U; ++k, r += TY) src[k] = r < r_hi ? lin_index(a.dy_rows, a.dy_total, r, a.err) : -1;
     };
-    auto source = [&](int r) { return r < r_hi ? lin_index(a.dy_rows, a.dy_total, r, a.err) : -1; };
-    int src = source(r_lo + ty);
+    auto load = [&](int r) {
+#pragma unroll
+        for (int k = 0; k < U; ++k, r += TY) {
+            if (!on || r >= r_hi) continue;
+            const size_t zi = static_cast<size_t>(r) * a.ldz + c;
+            dr[k] = LgRaw<VEC>{};
+            if (src[k] >= 0) lg_load<VEC>(a.dy, static_cast<size_t>(src[k]) * a.lddy + c, f32, dr[k]);
+            if (a.act != LACT_NONE) lg_load<VEC>(a.z[0], zi, false, zr[k]);
+            if (UP) lg_load<VEC>(a.z[1], zi, false, ur[k]);
+        }
+    };
+    source(r_lo + ty);
     if (AHEAD) {
-        load(r_lo + ty, src);
-        src = source(r_lo + ty + TY);
+        load(r_lo + ty);
+        source(r_lo + ty + U * TY);
     }
 #pragma unroll 1
-    for (int r = r_lo + ty; r < r_hi; r += TY) {
-        if (!AHEAD) load(r, src);
-        float dy[VEC], z[VEC], g[VEC], u[UP ? VEC : 1];
-        lg_values<VEC, TYPE>(dr, f32, dy);
-        lg_values<VEC, TYPE>(zr, false, z);
-        if constexpr (UP) lg_values<VEC, TYPE>(ur, false, u);
-        if (AHEAD) load(r + TY, src);
-        src = source(r + (AHEAD ? 2 : 1) * TY);
-        if (!on) continue;
-        const size_t gi = static_cast<size_t>(g0 + r) * a.lddz + c;
-        if constexpr (UP) {
+    for (int r0 = r_lo + ty; r0 < r_hi; r0 += U * TY) {
+        float dy[U][VEC], z[U][VEC], u[U][VEC];
+        if (!AHEAD) load(r0);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float sg = lin_sigmoid(z[i]);
-                g[i] = dy[i] * u[i] * (sg * (1.0f + z[i] * (1.0f - sg)));
-                u[i] = dy[i] * (z[i] * sg);
-                if (SUMS) {
-                    s0[i] += g[i];
-                    s1[i] += u[i];
+        for (int k = 0; k < U; ++k) {
+            lg_values<VEC, TYPE>(dr[k], f32, dy[k]);
+            lg_values<VEC, TYPE>(zr[k], false, z[k]);
+            if (UP) lg_values<VEC, TYPE>(ur[k], false, u[k]);
+        }
+        if (AHEAD) load(r0 + U * TY);
+        source(r0 + (AHEAD ? 2 : 1) * U * TY);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int r = r0 + k * TY;
+            if (!on || r >= r_hi) continue;
+            const size_t gi = static_cast<size_t>(g0 + r) * a.lddz + c;
+            float g[VEC];
+            if constexpr (UP) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float sg = lin_sigmoid(z[k][i]);
+                    g[i] = dy[k][i] * u[k][i] * (sg * (1.0f + z[k][i] * (1.0f - sg)));
+                    u[k][i] = dy[k][i] * (z[k][i] * sg);
+                    if (SUMS) {
+                        s0[i] += g[i];
+                        s1[i] += u[k][i];
+                    }
+                }
+                if (a.dz[1]) lg_store<VEC, TYPE>(a.dz[1], gi, u[k]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    g[i] = a.act == LACT_NONE ? dy[k][i] : dy[k][i] * lin_slope(a.act, z[k][i]);
+                    if (SUMS) s0[i] += g[i];
                 }
             }
-            if (a.dz[1]) lg_store<VEC, TYPE>(a.dz[1], gi, u);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                g[i] = a.act == LACT_NONE ? dy[i] : dy[i] * lin_slope(a.act, z[i]);
-                if (SUMS) s0[i] += g[i];
-            }
+            if (a.dz[0]) lg_store<VEC, TYPE>(a.dz[0], gi, g);
         }
-        if (a.dz[0]) lg_store<VEC, TYPE>(a.dz[0], gi, g);
     }
     if constexpr (SUMS) {
         if (!want_db) return;

@@ -1040,26 +1040,26 @@ cudaError_t lin_pack(moe_fp4_ctx* c, const LinCopies& k, void* scratch, const in
                     dim3(kLpThreads), 0, s, a);
 }
 
-template <int COLS>
+template <bool SUMS>
 void (*lin_grad_pick(bool vec, bool up, bool bf16))(LinGradArgs) {
     if (vec)
-        return up ? (bf16 ? lin_grad_kernel<8, true, LIN_BF16, COLS> : lin_grad_kernel<8, true, LIN_F16, COLS>)
-                  : (bf16 ? lin_grad_kernel<8, false, LIN_BF16, COLS> : lin_grad_kernel<8, false, LIN_F16, COLS>);
-    return up ? (bf16 ? lin_grad_kernel<1, true, LIN_BF16, COLS> : lin_grad_kernel<1, true, LIN_F16, COLS>)
-              : (bf16 ? lin_grad_kernel<1, false, LIN_BF16, COLS> : lin_grad_kernel<1, false, LIN_F16, COLS>);
+        return up ? (bf16 ? lin_grad_kernel<8, true, LIN_BF16, SUMS> : lin_grad_kernel<8, true, LIN_F16, SUMS>)
+                  : (bf16 ? lin_grad_kernel<8, false, LIN_BF16, SUMS> : lin_grad_kernel<8, false, LIN_F16, SUMS>);
+    return up ? (bf16 ? lin_grad_kernel<1, true, LIN_BF16, SUMS> : lin_grad_kernel<1, true, LIN_F16, SUMS>)
+              : (bf16 ? lin_grad_kernel<1, false, LIN_BF16, SUMS> : lin_grad_kernel<1, false, LIN_F16, SUMS>);
 }
 
 cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
     const bool db = g.db[0] || g.db[1], by_group = db || g.packed;
-    const bool wide = !db && g.N >= kLgWideCols;
-    const int cols = wide ? kLgWideCols : kLgSumCols, col_blocks = (g.N + cols - 1) / cols;
+    const bool sums = db || g.N < kLgWide;
     const int per_group = by_group ? (g.rows + g.E - 1) / g.E : g.rows;
     auto vec_ok = [](const void* p, long long ld, int type) {
         const uintptr_t step = type == LIN_F32 ? 4 : 8;
         return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % step == 0;
     };
-    bool vec = g.N % 8 == 0 && vec_ok(g.dy, g.lddy, g.dy_type) && vec_ok(g.dz[0], g.lddz, g.type) &&
+    const bool vec = g.N % 8 == 0 && vec_ok(g.dy, g.lddy, g.dy_type) && vec_ok(g.dz[0], g.lddz, g.type) &&
                vec_ok(g.dz[1], g.lddz, g.type) && vec_ok(g.z[0], g.ldz, g.type) && vec_ok(g.z[1], g.ldz, g.type);
+    const int cols = lg_cols(vec ? 8 : 1, sums), col_blocks = (g.N + cols - 1) / cols;
     // Strips of rows.  With db those of a group form a cluster (8 CTAs at most) and should hold enough rows for the
     // meeting of their sums to be small beside the loads.  Else 64 rows (8,192 x 2,304 SwiGLU: 37 us; 41 with 16, 40
     // with 256) or, as groups differ in size, 32 of an average group (12,288 rows in 64 groups, the largest six times
@@ -1090,7 +1090,7 @@ cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
     }
     const bool up = g.act == LACT_SWIGLU, bf16 = g.type == LIN_BF16;
     void (*const kernel)(LinGradArgs) =
-        wide ? lin_grad_pick<kLgWideCols>(vec, up, bf16) : lin_grad_pick<kLgSumCols>(vec, up, bf16);
+        sums ? lin_grad_pick<true>(vec, up, bf16) : lin_grad_pick<false>(vec, up, bf16);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, g);
     if (prof) {
         cudaEventRecord(eb, s);
