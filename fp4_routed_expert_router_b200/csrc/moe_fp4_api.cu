@@ -1060,13 +1060,19 @@ cudaError_t lin_grad_run(moe_fp4_ctx* c, const LinGradArgs& g, cudaStream_t s) {
     const bool vec = g.N % 8 == 0 && vec_ok(g.dy, g.lddy, g.dy_type) && vec_ok(g.dz[0], g.lddz, g.type) &&
                vec_ok(g.dz[1], g.lddz, g.type) && vec_ok(g.z[0], g.ldz, g.type) && vec_ok(g.z[1], g.ldz, g.type);
     const int cols = lg_cols(vec ? 8 : 1, sums), col_blocks = (g.N + cols - 1) / cols;
-    // Strips of rows.  With db those of a group form a cluster (8 CTAs at most) and should hold enough rows for the
-    // meeting of their sums to be small beside the loads.  Else 64 rows (8,192 x 2,304 SwiGLU: 37 us; 41 with 16, 40
-    // with 256) or, as groups differ in size, 32 of an average group (12,288 rows in 64 groups, the largest six times
-    // the average: 65 us; 92 with 64, 184 with 256).
-    int strips = db ? per_group / (vec ? 128 : 32) : (per_group + 63) / (by_group ? 32 : 64);
-    const int most = db ? 8 : 65535;
-    strips = strips < 1 ? 1 : strips > most ? most : strips;
+    // Strips of rows.  With db those of a group form a cluster (8 CTAs at most); more than two rounds of CTAs, or strips
+    // of a few rows, cost more in starting and in the meeting of their sums than they gain (7,120 x 4,089 in 22 groups:
+    // 518 us in 8 strips a group, 167 in one).  Else 64 rows (8,192 x 2,304 SwiGLU: 37 us; 41 with 16, 40 with 256) or,
+    // as groups differ in size, 32 of an average group (12,288 rows in 64 groups, the largest six times the average:
+    // 65 us; 92 with 64, 184 with 256).
+    int strips = (per_group + 63) / (by_group ? 32 : 64), most = 65535;
+    if (db) {
+        strips = per_group / (vec ? 128 : 32);
+        most = static_cast<int>(6LL * c->sm_count / (static_cast<long long>(col_blocks) * g.E));
+        if (most > 8) most = 8;
+    }
+    strips = strips > most ? most : strips;
+    if (strips < 1) strips = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(col_blocks), static_cast<unsigned>(strips),
                        static_cast<unsigned>(by_group ? g.E : 1));
